@@ -124,6 +124,53 @@ LMOE_API lmoe_status moe_route(const lmoe_dims* dims, const void* x, const void*
                       const float* expert_bias, int32_t* ids, float* probs, void* ws,
                       size_t ws_bytes, lmoe_stream stream);
 
+/* A routing rule with the experts in groups.
+ *   s     = sigmoid(l), or softmax of l over all R experts
+ *   key   = s + expert_bias (the bias only selects)
+ *   group = R / n_groups neighbouring experts; its score is the sum of its two
+ *           largest keys, or the largest
+ *   T     = the top_k largest keys among the topk_groups best groups, in
+ *           descending order
+ *   p_i   = scale * s_i / max(sum_T s, 1e-9) with renormalise, else scale * s_i
+ * Ties go to the lower group and the lower expert.  A key that is NaN ranks
+ * with -inf (so that the ids of a row are always k distinct experts); its
+ * weight stays NaN.  Logits of -inf have score 0, also where every logit of a
+ * row is -inf.  A bias of -inf closes an expert: it is chosen only when the
+ * kept groups hold fewer than k others. */
+typedef enum { LMOE_SCORE_SIGMOID = 0, LMOE_SCORE_SOFTMAX = 1 } lmoe_score;
+typedef enum { LMOE_GROUP_TOP2 = 0, LMOE_GROUP_MAX = 1 } lmoe_group_score;
+typedef struct {
+  int32_t score;       /* lmoe_score                                          */
+  int32_t n_groups;    /* divides n_routed; 1: no groups                      */
+  int32_t topk_groups; /* 1 .. n_groups, holding at least top_k experts       */
+  int32_t group_score; /* lmoe_group_score                                    */
+  int32_t renormalise; /* 0 or 1                                              */
+  float scale;         /* factor of the weights                               */
+} lmoe_route_rule;
+
+/* moe_route under a rule (dims->router is not used).  Arguments and workspace
+ * as for moe_route; the logits are left in the workspace. */
+LMOE_API lmoe_status moe_route_grouped(const lmoe_dims* dims, const lmoe_route_rule* rule,
+                                       const void* x, const void* w_router,
+                                       const float* expert_bias, int32_t* ids, float* probs,
+                                       void* ws, size_t ws_bytes, lmoe_stream stream);
+
+/* The same from given logits [N, ld] fp32 (ld >= R: their row stride), for a
+ * caller whose router product is its own. */
+LMOE_API lmoe_status moe_route_logits(const lmoe_dims* dims, const lmoe_route_rule* rule,
+                                      const float* logits, int64_t ld, const float* expert_bias,
+                                      int32_t* ids, float* probs, lmoe_stream stream);
+
+/* Its gradient: dlogits [N, ld_d] (R columns, every one written) of
+ * <dprobs, probs> for the routing ids [N, k] (each row k distinct experts, as
+ * the forward gives them; an id outside [0, R) adds nothing).  The choice of
+ * experts is not differentiated; where sum_T s is at its floor, the floor is a
+ * constant.  Deterministic. */
+LMOE_API lmoe_status moe_route_logits_backward(const lmoe_dims* dims, const lmoe_route_rule* rule,
+                                               const float* logits, int64_t ld, const int32_t* ids,
+                                               const float* dprobs, float* dlogits, int64_t ld_d,
+                                               lmoe_stream stream);
+
 /* Pair permutation (latent_moe.py LatentMoE._routed_u; sec-07 sparse dispatch,
  * step 1): the N*k (token, expert) pairs, flattened token-major, stably sorted
  * by expert id.  Bit-exact and deterministic.
@@ -167,6 +214,76 @@ LMOE_API lmoe_status moe_expert_ffn(const lmoe_dims* dims, const void* z, const 
                            const int32_t* offsets, const void* w_g, const void* w_u,
                            const void* w_o, void* expert_out, void* ws, size_t ws_bytes,
                            lmoe_stream stream);
+
+/* ---- 8-bit routed experts -------------------------------------------------
+ * e4m3 values with one power-of-two scale (E8M0) for each block of 128: the
+ * tensor cores of this GPU apply such scales themselves.  A block's scale is
+ * 2^e with the smallest e >= -126 for which its largest finite magnitude is at
+ * most 448 scales (448: the largest e4m3 value), stored as the byte e + 127;
+ * a block of zeros has scale 1.  An element is x * 2^-e rounded to nearest
+ * even; a NaN or an infinity becomes NaN.
+ *   rows    [n, c]:    blocks of 128 columns of a row;
+ *           scales [ceil(c / 512), n, 4]: block b of row r at [b / 4, r, b % 4]
+ *   weights [m, r, c]: blocks of 128 x 128, the last ones smaller;
+ *           scales [m, ceil(r / 128), 4 ceil(c / 512)]
+ * Bytes past the last block of c are 127.  c is a multiple of 16. */
+
+/* Quantises rows.  x [n_src, cols] of dtype (lmoe_dtype), row stride ld
+ * elements (rows 16-byte aligned); q [rows, cols] and scales out.  With index
+ * [rows], row r is x[index[r]], and a row of zeros where index[r] is outside
+ * [0, n_src) (the rows of perm_token behind the last sorted pair); without,
+ * n_src = rows. */
+LMOE_API lmoe_status lmoe_quantize_rows_fp8(const void* x, int32_t dtype, int64_t n_src, int64_t ld,
+                                            const int32_t* index, int64_t rows, int32_t cols,
+                                            void* q, uint8_t* scales, lmoe_stream stream);
+
+/* Quantises n_mats stacked matrices w [n_mats, rows, cols] of dtype to q (same
+ * shape) and scales.  The blocks are square, so the transposed matrices have
+ * the transposed values and scales. */
+LMOE_API lmoe_status lmoe_quantize_weights_fp8(const void* w, int32_t dtype, int64_t n_mats,
+                                               int64_t rows, int32_t cols, void* q, uint8_t* scales,
+                                               lmoe_stream stream);
+
+/* Product of quantised rows with the quantised weights of their expert: for
+ * each expert e and row r in [offsets[e], offsets[e + 1]),
+ *   out[r, j] = sum_i A[r, i] W_e[j, i]     (fp32 accumulation)
+ * A and W the values that a, w and their scales stand for.
+ *   a [N*k, n_in], a_scales: as lmoe_quantize_rows_fp8 writes them
+ *   offsets [R+1] from moe_dispatch, or NULL when n_routed = 1: all rows
+ *   w [R, n_out, n_in], w_scales: as lmoe_quantize_weights_fp8 writes them
+ *   out [N*k, n_out] in the activation dtype; rows in no expert's range are
+ *   left as they are
+ * n_in a multiple of 16, n_out of 8.  Offsets are clamped to an ascending
+ * order in [0, N*k].  With the transposed weights and scales it gives the
+ * gradient of the rows (the weights being constants).  Workspace:
+ * lmoe_workspace_size(dims) bytes (of dims: n_tokens, top_k, n_routed, dtype
+ * matter here). */
+LMOE_API lmoe_status moe_expert_gemm_fp8(const lmoe_dims* dims, int32_t n_in, int32_t n_out,
+                                         const void* a, const uint8_t* a_scales,
+                                         const int32_t* offsets, const void* w,
+                                         const uint8_t* w_scales, void* out, void* ws,
+                                         size_t ws_bytes, lmoe_stream stream);
+
+/* Quantised weights of the routed experts (lmoe_quantize_weights_fp8). */
+typedef struct {
+  const void* w_g;             /* [R, F, l] */
+  const uint8_t* w_g_scales;
+  const void* w_u;             /* [R, F, l] */
+  const uint8_t* w_u_scales;
+  const void* w_o;             /* [R, l, F] */
+  const uint8_t* w_o_scales;
+} lmoe_fp8_experts;
+
+/* moe_expert_ffn with 8-bit products: the rows z[perm_token[r]] are quantised,
+ * a and c are products with W_g and W_u, the hidden units (in fp32) are
+ * quantised, and expert_out is the product with W_o, in the activation dtype.
+ * Rows in no expert's range are left as they are.  latent and ff_routed
+ * multiples of 16.  z, perm_token, offsets, expert_out and the workspace as
+ * for moe_expert_ffn. */
+LMOE_API lmoe_status moe_expert_ffn_fp8(const lmoe_dims* dims, const void* z,
+                                        const int32_t* perm_token, const int32_t* offsets,
+                                        const lmoe_fp8_experts* weights, void* expert_out, void* ws,
+                                        size_t ws_bytes, lmoe_stream stream);
 
 /* Weighted combine + RMSNorm (latent_moe.py index_add and self.norm; sec-07
  * step 3 sum and step 5 RMSNorm): for each token t, in slot order,
@@ -358,7 +475,7 @@ LMOE_API const char* lmoe_last_error(void);
  * the side stream back into its own stream before it returns, so a stream
  * capture of the call stays closed.  Tags: "xpass", "route", "dispatch",
  * "gather", "expert_gemm1", "expert_gemm2", "combine", "final",
- * "router_losses". */
+ * "router_losses", "route_backward", "quantize", "expert_gemm". */
 LMOE_API lmoe_status lmoe_profile_enable(const char* tags);
 /* Waits for the recorded events of kernel `tag` (NULL: every tag); returns the
  * summed device time (ms) and the number of bracketed launches since the last

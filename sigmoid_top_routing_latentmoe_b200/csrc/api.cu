@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "experts_fp8.h"
 #include "kernels.h"
 #include "umma_gemm.h"
 
@@ -255,21 +256,13 @@ static lmoe_status check_ws(const lmoe_dims* d, void* ws, size_t ws_bytes, bool 
   } while (0)
 
 // ------------------------------------------------------------- launchers
+// Router logits of R > 32 experts, left in the workspace.
 template <typename T>
-static lmoe_status run_route(const lmoe_dims* d, const void* x, const void* w_r, const float* bias,
-                             int32_t* ids, float* probs, void* ws, cudaStream_t st) {
+static lmoe_status run_logits(const lmoe_dims* d, const void* x, const void* w_r, void* ws,
+                              cudaStream_t st) {
   const Layout L = layout(d, false);
   const int64_t N = d->n_tokens;
-  if (N == 0) return LMOE_OK;
   float* logits = at<float>(ws, L.logits);
-  if (d->n_routed <= 32) {
-    ProfScope ps("route", st);
-    LMOE_CUDA(launch_route_gemv<T>((const T*)x, (const T*)w_r, bias, N, d->d, d->n_routed,
-                                   d->top_k, d->router, ids, probs, logits, L.logits_ld, st),
-              "route_gemv");
-    return LMOE_OK;
-  }
-  ProfScope ps("route", st);
   if (std::is_same<T, __nv_bfloat16>::value) {
     XpassArgs a{};
     a.x = (const __nv_bfloat16*)x; a.N = N; a.d = d->d; a.L = 0; a.w_router = (const __nv_bfloat16*)w_r;
@@ -283,9 +276,100 @@ static lmoe_status run_route(const lmoe_dims* d, const void* x, const void* w_r,
     g.mode = kStore;
     LMOE_CUDA(launch_simt_gemm<T>(g, st), "router logits");
   }
+  return LMOE_OK;
+}
+
+template <typename T>
+static lmoe_status run_route(const lmoe_dims* d, const void* x, const void* w_r, const float* bias,
+                             int32_t* ids, float* probs, void* ws, cudaStream_t st) {
+  const Layout L = layout(d, false);
+  const int64_t N = d->n_tokens;
+  if (N == 0) return LMOE_OK;
+  float* logits = at<float>(ws, L.logits);
+  ProfScope ps("route", st);
+  if (d->n_routed <= 32) {
+    LMOE_CUDA(launch_route_gemv<T>((const T*)x, (const T*)w_r, bias, N, d->d, d->n_routed,
+                                   d->top_k, d->router, ids, probs, logits, L.logits_ld, st),
+              "route_gemv");
+    return LMOE_OK;
+  }
+  LMOE_TRY(run_logits<T>(d, x, w_r, ws, st));
   LMOE_CUDA(launch_route_topk(logits, L.logits_ld, bias, N, d->n_routed, d->top_k, d->router, ids,
                               probs, st),
             "route_topk");
+  return LMOE_OK;
+}
+
+// Routing under a rule: the logits as moe_route computes them (for R <= 32
+// together with its own ids and probs, which the rule's then replace).
+template <typename T>
+static lmoe_status run_route_grouped(const lmoe_dims* d, const RouteRule& rule, const void* x,
+                                     const void* w_r, const float* bias, int32_t* ids,
+                                     float* probs, void* ws, cudaStream_t st) {
+  if (d->n_tokens == 0) return LMOE_OK;
+  const Layout L = layout(d, false);
+  if (d->n_routed <= 32) LMOE_TRY(run_route<T>(d, x, w_r, nullptr, ids, probs, ws, st));
+  else LMOE_TRY(run_logits<T>(d, x, w_r, ws, st));
+  ProfScope ps("route", st);
+  LMOE_CUDA(launch_route_rule(rule, at<float>(ws, L.logits), L.logits_ld, bias, d->n_tokens,
+                              d->n_routed, d->top_k, ids, probs, st),
+            "route rule");
+  return LMOE_OK;
+}
+
+// ------------------------------------------------------- 8-bit routed experts
+static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* offsets, void* ws) {
+  TileList t;
+  t.offsets = offsets; t.R = d->n_routed; t.rows = d->n_tokens * d->top_k;
+  t.max_tiles = L.max_tiles;
+  t.n_mtiles = &at<WsHeader>(ws, L.header)->n_mtiles;
+  t.tiles = at<int4>(ws, L.tiles);
+  return t;
+}
+
+// Rows of z quantised in sorted order, gate and up products with the SiTU and
+// the quantisation of the hidden units in their epilogue, output product.  The
+// quantised rows take the first half of the workspace's sorted-row area (which
+// holds rows of 2 or 4 bytes an element) and their scales the second; the
+// hidden units likewise.
+template <typename T>
+static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const int32_t* perm,
+                                      const int32_t* offsets, const lmoe_fp8_experts* w, void* out,
+                                      void* ws, cudaStream_t st) {
+  const Layout L = layout(d, false);
+  const int64_t P = d->n_tokens * d->top_k;
+  if (P == 0) return LMOE_OK;
+  const int Lt = d->latent, F = d->ff_routed;
+  uint8_t* zq = at<uint8_t>(ws, L.zp);
+  uint8_t* zs = zq + P * Lt;
+  uint8_t* hq = at<uint8_t>(ws, L.h);
+  uint8_t* hs = hq + P * F;
+  const TileList tl = tile_list(d, L, offsets, ws);
+  int32_t* status = &at<WsHeader>(ws, L.header)->status;
+  {
+    ProfScope ps("quantize", st);
+    LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");
+    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, perm, P, Lt, zq, zs, st),
+              "quantize rows");
+  }
+  Fp8Gemm g{};
+  g.rows = P; g.R = d->n_routed; g.tiles = tl.tiles; g.n_mtiles = tl.n_mtiles;
+  g.max_tiles = tl.max_tiles; g.beta1 = d->beta1; g.beta2 = d->beta2;
+  {
+    ProfScope ps("expert_gemm1", st);
+    g.a = zq; g.a_scales = zs; g.n_in = Lt; g.n_out = F; g.situ = 1;
+    g.w = (const uint8_t*)w->w_g; g.w_scales = w->w_g_scales;
+    g.w_up = (const uint8_t*)w->w_u; g.w_up_scales = w->w_u_scales;
+    g.out = hq; g.out_scales = hs;
+    LMOE_CUDA(launch_fp8_gemm(g, status, st), "routed gemm1 (8-bit)");
+  }
+  {
+    ProfScope ps("expert_gemm2", st);
+    g.a = hq; g.a_scales = hs; g.n_in = F; g.n_out = Lt; g.situ = 0;
+    g.w = (const uint8_t*)w->w_o; g.w_scales = w->w_o_scales;
+    g.out = out; g.out_f32 = std::is_same<T, float>::value ? 1 : 0;
+    LMOE_CUDA(launch_fp8_gemm(g, status, st), "routed gemm2 (8-bit)");
+  }
   return LMOE_OK;
 }
 
@@ -797,6 +881,254 @@ lmoe_status moe_expert_ffn(const lmoe_dims* dims, const void* z, const int32_t* 
     return run_expert_ffn<__nv_bfloat16>(dims, z, perm_token, offsets, w_g, w_u, w_o, expert_out,
                                          ws, st);
   return run_expert_ffn<float>(dims, z, perm_token, offsets, w_g, w_u, w_o, expert_out, ws, st);
+}
+
+// ------------------------------------------------------- routing under a rule
+static lmoe_status check_rule(const lmoe_dims* d, const lmoe_route_rule* r, RouteRule* out) {
+  if (r == nullptr) return fail(LMOE_EINVAL, "rule is NULL");
+  if (r->score != LMOE_SCORE_SIGMOID && r->score != LMOE_SCORE_SOFTMAX)
+    return fail(LMOE_EINVAL, "score %d", r->score);
+  if (r->group_score != LMOE_GROUP_TOP2 && r->group_score != LMOE_GROUP_MAX)
+    return fail(LMOE_EINVAL, "group_score %d", r->group_score);
+  if (r->renormalise != 0 && r->renormalise != 1)
+    return fail(LMOE_EINVAL, "renormalise %d", r->renormalise);
+  if (r->n_groups < 1 || d->n_routed % r->n_groups != 0)
+    return fail(LMOE_EINVAL, "n_groups %d does not divide n_routed %d", r->n_groups, d->n_routed);
+  if (r->topk_groups < 1 || r->topk_groups > r->n_groups)
+    return fail(LMOE_EINVAL, "topk_groups out of [1, n_groups]");
+  if (r->topk_groups * (d->n_routed / r->n_groups) < d->top_k)
+    return fail(LMOE_EINVAL, "%d groups of %d experts hold fewer than top_k = %d", r->topk_groups,
+                d->n_routed / r->n_groups, d->top_k);
+  if (!std::isfinite(r->scale)) return fail(LMOE_EINVAL, "scale is not finite");
+  out->softmax = r->score == LMOE_SCORE_SOFTMAX;
+  out->n_groups = r->n_groups;
+  out->topk_groups = r->topk_groups;
+  out->top2 = r->group_score == LMOE_GROUP_TOP2;
+  out->renormalise = r->renormalise;
+  out->scale = r->scale;
+  return LMOE_OK;
+}
+
+static lmoe_status check_logits(const lmoe_dims* d, const void* logits, int64_t ld,
+                                const char* name) {
+  if (d->n_tokens == 0) return LMOE_OK;
+  if (logits == nullptr) return fail(LMOE_EINVAL, "%s is NULL", name);
+  if (ld < d->n_routed || (uintptr_t)logits % 4 != 0)
+    return fail(LMOE_EINVAL, "%s: row stride < n_routed or misaligned", name);
+  return LMOE_OK;
+}
+
+lmoe_status moe_route_grouped(const lmoe_dims* dims, const lmoe_route_rule* rule, const void* x,
+                              const void* w_router, const float* expert_bias, int32_t* ids,
+                              float* probs, void* ws, size_t ws_bytes, lmoe_stream stream) {
+  LMOE_TRY(check_dims(dims));
+  RouteRule r;
+  LMOE_TRY(check_rule(dims, rule, &r));
+  if (dims->n_tokens > 0) {
+    LMOE_PTR(x, "x");
+    LMOE_PTR(ids, "ids");
+    LMOE_PTR(probs, "probs");
+  }
+  LMOE_PTR(w_router, "w_router");
+  if (expert_bias != nullptr && !aligned16(expert_bias))
+    return fail(LMOE_EINVAL, "expert_bias is not 16-byte aligned");
+  LMOE_TRY(check_ws(dims, ws, ws_bytes, false));
+  LMOE_TRY(check_device());
+  ProfJoin pj((cudaStream_t)stream);  // joins the profiling branch on return
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dims->dtype == LMOE_BF16)
+    return run_route_grouped<__nv_bfloat16>(dims, r, x, w_router, expert_bias, ids, probs, ws, st);
+  return run_route_grouped<float>(dims, r, x, w_router, expert_bias, ids, probs, ws, st);
+}
+
+lmoe_status moe_route_logits(const lmoe_dims* dims, const lmoe_route_rule* rule,
+                             const float* logits, int64_t ld, const float* expert_bias,
+                             int32_t* ids, float* probs, lmoe_stream stream) {
+  LMOE_TRY(check_dims(dims));
+  RouteRule r;
+  LMOE_TRY(check_rule(dims, rule, &r));
+  LMOE_TRY(check_logits(dims, logits, ld, "logits"));
+  if (dims->n_tokens > 0) {
+    LMOE_PTR(ids, "ids");
+    LMOE_PTR(probs, "probs");
+  }
+  if (expert_bias != nullptr && !aligned16(expert_bias))
+    return fail(LMOE_EINVAL, "expert_bias is not 16-byte aligned");
+  LMOE_TRY(check_device());
+  ProfJoin pj((cudaStream_t)stream);  // joins the profiling branch on return
+  ProfScope ps("route", (cudaStream_t)stream);
+  LMOE_CUDA(launch_route_rule(r, logits, ld, expert_bias, dims->n_tokens, dims->n_routed,
+                              dims->top_k, ids, probs, (cudaStream_t)stream),
+            "route rule");
+  return LMOE_OK;
+}
+
+lmoe_status moe_route_logits_backward(const lmoe_dims* dims, const lmoe_route_rule* rule,
+                                      const float* logits, int64_t ld, const int32_t* ids,
+                                      const float* dprobs, float* dlogits, int64_t ld_d,
+                                      lmoe_stream stream) {
+  LMOE_TRY(check_dims(dims));
+  RouteRule r;
+  LMOE_TRY(check_rule(dims, rule, &r));
+  LMOE_TRY(check_logits(dims, logits, ld, "logits"));
+  LMOE_TRY(check_logits(dims, dlogits, ld_d, "dlogits"));
+  if (dims->n_tokens > 0) {
+    LMOE_PTR(ids, "ids");
+    LMOE_PTR(dprobs, "dprobs");
+  }
+  LMOE_TRY(check_device());
+  ProfJoin pj((cudaStream_t)stream);  // joins the profiling branch on return
+  ProfScope ps("route_backward", (cudaStream_t)stream);
+  LMOE_CUDA(launch_route_rule_backward(r, logits, ld, ids, dprobs, dims->n_tokens, dims->n_routed,
+                                       dims->top_k, dlogits, ld_d, (cudaStream_t)stream),
+            "route rule backward");
+  return LMOE_OK;
+}
+
+// --------------------------------------------------------- 8-bit routed experts
+constexpr int64_t kFp8MaxWidth = 1 << 20;
+static lmoe_status check_fp8_width(int64_t cols, const char* name) {
+  if (cols < 16 || cols % 16 != 0 || cols > kFp8MaxWidth)
+    return fail(LMOE_EINVAL, "%s = %lld: 8-bit rows are multiples of 16 up to 2^20", name,
+                (long long)cols);
+  return LMOE_OK;
+}
+
+lmoe_status lmoe_quantize_rows_fp8(const void* x, int32_t dtype, int64_t n_src, int64_t ld,
+                                   const int32_t* index, int64_t rows, int32_t cols, void* q,
+                                   uint8_t* scales, lmoe_stream stream) {
+  if (dtype != LMOE_F32 && dtype != LMOE_BF16) return fail(LMOE_EINVAL, "dtype %d", dtype);
+  LMOE_TRY(check_fp8_width(cols, "cols"));
+  if (rows < 0 || n_src < 0 || rows >= ((int64_t)1 << 31) || n_src >= ((int64_t)1 << 31))
+    return fail(LMOE_EINVAL, "rows or n_src out of [0, 2^31)");
+  if (index == nullptr && n_src != rows)
+    return fail(LMOE_EINVAL, "n_src must equal rows without an index");
+  const int es = dtype == LMOE_BF16 ? 2 : 4;
+  if (ld < cols || ld * es % 16 != 0)
+    return fail(LMOE_EINVAL, "ld: rows overlap or are not 16-byte aligned");
+  if (rows == 0) return LMOE_OK;
+  if (n_src > 0) LMOE_PTR(x, "x");
+  if (index != nullptr && (uintptr_t)index % 4 != 0)
+    return fail(LMOE_EINVAL, "index is not 4-byte aligned");
+  LMOE_PTR(q, "q");
+  LMOE_PTR(scales, "scales");
+  LMOE_TRY(check_device());
+  cudaStream_t st = (cudaStream_t)stream;
+  ProfJoin pj(st);  // joins the profiling branch on return
+  ProfScope ps("quantize", st);
+  if (dtype == LMOE_BF16)
+    LMOE_CUDA(launch_quantize_rows<__nv_bfloat16>((const __nv_bfloat16*)x, n_src, ld, index, rows,
+                                                  cols, (uint8_t*)q, scales, st),
+              "quantize rows");
+  else
+    LMOE_CUDA(launch_quantize_rows<float>((const float*)x, n_src, ld, index, rows, cols,
+                                          (uint8_t*)q, scales, st),
+              "quantize rows");
+  return LMOE_OK;
+}
+
+lmoe_status lmoe_quantize_weights_fp8(const void* w, int32_t dtype, int64_t n_mats, int64_t rows,
+                                      int32_t cols, void* q, uint8_t* scales, lmoe_stream stream) {
+  if (dtype != LMOE_F32 && dtype != LMOE_BF16) return fail(LMOE_EINVAL, "dtype %d", dtype);
+  LMOE_TRY(check_fp8_width(cols, "cols"));
+  if (n_mats < 0 || rows < 1 || rows > kFp8MaxWidth || n_mats >= ((int64_t)1 << 31))
+    return fail(LMOE_EINVAL, "n_mats or rows out of range");
+  if (n_mats * q_blocks(rows) * q_words(cols) >= ((int64_t)1 << 29))
+    return fail(LMOE_EUNSUPPORTED, "too many blocks in one call");
+  if (n_mats == 0) return LMOE_OK;
+  LMOE_PTR(w, "w");
+  LMOE_PTR(q, "q");
+  LMOE_PTR(scales, "scales");
+  LMOE_TRY(check_device());
+  cudaStream_t st = (cudaStream_t)stream;
+  ProfJoin pj(st);  // joins the profiling branch on return
+  ProfScope ps("quantize", st);
+  if (dtype == LMOE_BF16)
+    LMOE_CUDA(launch_quantize_weights<__nv_bfloat16>((const __nv_bfloat16*)w, n_mats, rows, cols,
+                                                     (uint8_t*)q, scales, st),
+              "quantize weights");
+  else
+    LMOE_CUDA(launch_quantize_weights<float>((const float*)w, n_mats, rows, cols, (uint8_t*)q,
+                                             scales, st),
+              "quantize weights");
+  return LMOE_OK;
+}
+
+// Tiles of a product must be counted in 31 bits.
+static lmoe_status check_fp8_tiles(const lmoe_dims* d, int64_t n_out) {
+  if (layout(d, false).max_tiles * ((n_out + kQBlock - 1) / kQBlock) >= ((int64_t)1 << 31) - 4096)
+    return fail(LMOE_EUNSUPPORTED, "too many rows x columns in one product");
+  return LMOE_OK;
+}
+
+lmoe_status moe_expert_gemm_fp8(const lmoe_dims* dims, int32_t n_in, int32_t n_out, const void* a,
+                                const uint8_t* a_scales, const int32_t* offsets, const void* w,
+                                const uint8_t* w_scales, void* out, void* ws, size_t ws_bytes,
+                                lmoe_stream stream) {
+  LMOE_TRY(check_dims(dims));
+  LMOE_TRY(check_fp8_width(n_in, "n_in"));
+  if (n_out < 8 || n_out % 8 != 0 || n_out > kFp8MaxWidth)
+    return fail(LMOE_EINVAL, "n_out = %d: a multiple of 8 up to 2^20", n_out);
+  LMOE_TRY(check_fp8_tiles(dims, n_out));
+  if (dims->n_tokens > 0) {
+    LMOE_PTR(a, "a");
+    LMOE_PTR(a_scales, "a_scales");
+    LMOE_PTR(out, "out");
+  }
+  if (offsets == nullptr) {
+    if (dims->n_routed != 1) return fail(LMOE_EINVAL, "offsets is NULL with n_routed > 1");
+  } else {
+    LMOE_PTR(offsets, "offsets");
+  }
+  LMOE_PTR(w, "w");
+  LMOE_PTR(w_scales, "w_scales");
+  LMOE_TRY(check_ws(dims, ws, ws_bytes, false));
+  LMOE_TRY(check_device());
+  cudaStream_t st = (cudaStream_t)stream;
+  ProfJoin pj(st);  // joins the profiling branch on return
+  if (dims->n_tokens == 0) return LMOE_OK;
+  const Layout L = layout(dims, false);
+  const TileList tl = tile_list(dims, L, offsets, ws);
+  Fp8Gemm g{};
+  g.a = (const uint8_t*)a; g.a_scales = a_scales; g.rows = tl.rows; g.R = dims->n_routed;
+  g.n_in = n_in; g.n_out = n_out; g.w = (const uint8_t*)w; g.w_scales = w_scales; g.out = out;
+  g.out_f32 = dims->dtype == LMOE_F32 ? 1 : 0;
+  if (offsets != nullptr) {
+    g.tiles = tl.tiles; g.n_mtiles = tl.n_mtiles; g.max_tiles = tl.max_tiles;
+    LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");
+  }
+  ProfScope ps("expert_gemm", st);
+  LMOE_CUDA(launch_fp8_gemm(g, &at<WsHeader>(ws, L.header)->status, st), "expert gemm (8-bit)");
+  return LMOE_OK;
+}
+
+lmoe_status moe_expert_ffn_fp8(const lmoe_dims* dims, const void* z, const int32_t* perm_token,
+                               const int32_t* offsets, const lmoe_fp8_experts* w, void* expert_out,
+                               void* ws, size_t ws_bytes, lmoe_stream stream) {
+  LMOE_TRY(check_dims(dims));
+  LMOE_TRY(check_fp8_width(dims->latent, "latent"));
+  LMOE_TRY(check_fp8_width(dims->ff_routed, "ff_routed"));
+  LMOE_TRY(check_fp8_tiles(dims, std::max(dims->latent, dims->ff_routed)));
+  if (w == nullptr) return fail(LMOE_EINVAL, "weights is NULL");
+  if (dims->n_tokens > 0) {
+    LMOE_PTR(z, "z");
+    LMOE_PTR(perm_token, "perm_token");
+    LMOE_PTR(expert_out, "expert_out");
+  }
+  LMOE_PTR(offsets, "offsets");
+  LMOE_PTR(w->w_g, "w_g");
+  LMOE_PTR(w->w_u, "w_u");
+  LMOE_PTR(w->w_o, "w_o");
+  LMOE_PTR(w->w_g_scales, "w_g_scales");
+  LMOE_PTR(w->w_u_scales, "w_u_scales");
+  LMOE_PTR(w->w_o_scales, "w_o_scales");
+  LMOE_TRY(check_ws(dims, ws, ws_bytes, false));
+  LMOE_TRY(check_device());
+  cudaStream_t st = (cudaStream_t)stream;
+  ProfJoin pj(st);  // joins the profiling branch on return
+  if (dims->dtype == LMOE_BF16)
+    return run_expert_ffn_fp8<__nv_bfloat16>(dims, z, perm_token, offsets, w, expert_out, ws, st);
+  return run_expert_ffn_fp8<float>(dims, z, perm_token, offsets, w, expert_out, ws, st);
 }
 
 lmoe_status lmoe_check_dispatch(const lmoe_dims* dims, const int32_t* ids, const int32_t* counts,

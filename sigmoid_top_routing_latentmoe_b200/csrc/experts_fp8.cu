@@ -1,0 +1,516 @@
+// Ragged e4m3 products of the routed experts with a power-of-two scale for
+// each 128 elements of K (rows) and each 128 x 128 block (weights):
+//   out[r, n] = sum_b 2^(ea[r, b] + ew[n / 128, b]) sum_{k in b} a[r, k] w[n, k].
+// The tensor cores apply the scales themselves (kind::mxf8f6f4, one E8M0 byte
+// for 32 elements of K: a block's byte serves its four K steps), so the sum
+// over all of K stays in one fp32 TMEM accumulator.
+//
+// One persistent, warp-specialised kernel; a tile is 128 rows of one expert x
+// 256 columns (SiTU: 128 gate and the 128 matching up columns), K in blocks of
+// 128 (one 128-byte swizzle row):
+//   warp 0     TMA producer: A rows and two 128-row B boxes per K block,
+//   warp 1     MMA issuer and TMEM allocator; every fourth K block it also
+//              copies the next four blocks' scale words to TMEM,
+//   warp 2     scale producer: the words of four K blocks (128 rows of A, one
+//              or two weight blocks) in the order tcgen05.cp wants,
+//   warps 3-10 epilogue, two per 32-row quarter, each taking half the columns.
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "experts_fp8.h"
+#include "kernels.h"
+#include "launch.h"
+#include "quantize.cuh"
+#include "tc_ptx.cuh"
+
+namespace lmoe {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128, SUB = 128, BK = 128;
+constexpr int A_BYTES = BM * BK, B_BYTES = 2 * SUB * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = 4;
+constexpr int SMALL_ROWS = 32;            // tiles of at most this many rows load a smaller A box
+constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
+constexpr int SF_BYTES = 3 * 512;         // A words, then two blocks of B words
+constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
+constexpr int EPI_WARPS = 8, EPI_WARP0 = 3, EPI_STAGE = 32 * 64;  // 32 rows x 64 bytes per warp
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int SMEM_BYTES =
+    STAGES * STAGE_BYTES + EPI_WARPS * EPI_STAGE + SF_STAGES * SF_BYTES + 1024;
+constexpr int TMEM_COLS = 512, SF_COL0 = 256;
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+static_assert(SF_COL0 + SF_STAGES * SF_COLS <= TMEM_COLS, "TMEM");
+
+enum Out { OUT_BF16 = 0, OUT_F32 = 1, OUT_SITU = 2 };
+
+struct Params {
+  CUtensorMap tmA, tmA32, tmB0, tmB1;
+  const uint32_t* a_words;               // [words, rows]
+  const uint32_t *w_words, *w_up_words;  // [R, w_blocks, words]
+  int rows, words, w_blocks, kb, n_tiles, n_out;
+  const int4* tiles;
+  const int32_t* n_mtiles;
+  void* out;
+  uint8_t* out_scales;
+  int32_t* status;
+  float beta1, beta2;
+};
+
+struct Tile {
+  int e, m0, rows, n;
+};
+__device__ __forceinline__ int total_tiles(const Params& p) {
+  return (p.tiles != nullptr ? *p.n_mtiles : (p.rows + BM - 1) / BM) * p.n_tiles;
+}
+__device__ __forceinline__ Tile decode_tile(const Params& p, int t) {
+  const int mt = t / p.n_tiles, n = t - mt * p.n_tiles;
+  if (p.tiles == nullptr) return {0, mt * BM, min(BM, p.rows - mt * BM), n};
+  const int4 e = p.tiles[mt];
+  return {e.x, e.y, e.z, n};
+}
+// Whether a plain tile has a second 128-column half.
+template <int OUT>
+__device__ __forceinline__ bool two_subs(const Params& p, const Tile& tl) {
+  return OUT == OUT_SITU || tl.n * 2 * SUB + SUB < p.n_out;
+}
+
+struct Sync {
+  uint64_t full[STAGES], empty[STAGES], sfull[SF_STAGES], sempty[SF_STAGES], tfull, tempty, drain,
+      pair[4];
+  float amax[2][EPI_WARPS][32];
+  uint32_t tmem;
+  volatile int abort_flag;
+};
+
+template <int OUT>
+__device__ void produce(const Params& p, uint32_t ring, Sync& s) {
+  int stage = 0;
+  uint32_t phase = 0, issued = 0, issued_phase = 0;
+  bool ok = true;
+  const int total = total_tiles(p);
+  for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+    const Tile tl = decode_tile(p, t);
+    const bool small = tl.rows <= SMALL_ROWS, two = two_subs<OUT>(p, tl);
+    const CUtensorMap* map_a = small ? &p.tmA32 : &p.tmA;
+    const CUtensorMap* map_b1 = OUT == OUT_SITU ? &p.tmB1 : &p.tmB0;
+    const int row0 = OUT == OUT_SITU ? tl.n * SUB : tl.n * 2 * SUB;
+    const int row1 = OUT == OUT_SITU ? row0 : row0 + SUB;
+    const uint32_t bytes =
+        (small ? SMALL_ROWS * BK : A_BYTES) + (two ? B_BYTES : B_BYTES / 2);
+    for (int kb = 0; kb < p.kb; ++kb) {
+      if (!mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, &s.abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dst = ring + stage * STAGE_BYTES, bar = smem_u32(&s.full[stage]);
+      mbar_expect_tx(bar, bytes);
+      tma_load_2d(dst, map_a, bar, kb * BK, tl.m0);
+      tma_load_3d(dst + A_BYTES, &p.tmB0, bar, kb * BK, row0, tl.e);
+      if (two) tma_load_3d(dst + A_BYTES + SUB * BK, map_b1, bar, kb * BK, row1, tl.e);
+      issued |= 1u << stage;
+      issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+  // every load issued has landed before the block exits
+  for (int i = 0; i < STAGES; ++i)
+    if (issued & (1u << i)) {
+      volatile int no_abort = 0;
+      mbar_wait(smem_u32(&s.full[i]), (issued_phase >> i) & 1u, &no_abort, p.status);
+    }
+}
+
+// Scale words of four K blocks: row r of A at byte (r % 32) * 16 + (r / 32) * 4,
+// so that tcgen05.cp puts it in lane r % 32, column r / 32; a weight block has
+// one word for its 128 rows.
+template <int OUT>
+__device__ void produce_scales(const Params& p, uint32_t sf, Sync& s) {
+  const int lane = threadIdx.x & 31;
+  int stage = 0;
+  uint32_t phase = 0;
+  const int total = total_tiles(p);
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    const Tile tl = decode_tile(p, t);
+    const bool two = two_subs<OUT>(p, tl);
+    const int nb0 = OUT == OUT_SITU ? tl.n : 2 * tl.n;
+    const uint32_t* w0 = p.w_words + ((int64_t)tl.e * p.w_blocks + nb0) * p.words;
+    const uint32_t* w1 =
+        OUT == OUT_SITU ? p.w_up_words + ((int64_t)tl.e * p.w_blocks + nb0) * p.words : w0 + p.words;
+    for (int q = 0; q < p.words; ++q) {
+      uint32_t a[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = lane + 32 * j;  // words of rows past the tile scale rows never stored
+        a[j] = r < tl.rows ? p.a_words[(int64_t)q * p.rows + tl.m0 + r] : 0u;
+      }
+      const uint32_t b0 = w0[q], b1 = two ? w1[q] : 0u;
+      if (!warp_wait(smem_u32(&s.sempty[stage]), phase ^ 1u, &s.abort_flag, p.status)) return;
+      const uint32_t dst = sf + stage * SF_BYTES + lane * 16;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a[0]), "r"(a[1]),
+                   "r"(a[2]), "r"(a[3])
+                   : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + 512), "r"(b0) : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + 1024), "r"(b1) : "memory");
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.sfull[stage]));
+      if (++stage == SF_STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+}
+
+template <int OUT>
+__device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t sf, uint32_t tmem, Sync& s) {
+  int stage = 0, sstage = 0;
+  uint32_t phase = 0, sphase = 0, tphase = 0;
+  bool ok = true;
+  const int total = total_tiles(p);
+  for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+    const Tile tl = decode_tile(p, t);
+    const bool two = two_subs<OUT>(p, tl);
+    const uint32_t idesc = instr_desc_mxf8(two ? 2 * SUB : SUB);
+    if (!mbar_wait(smem_u32(&s.tempty), tphase ^ 1u, &s.abort_flag, p.status)) break;
+    tphase ^= 1u;
+    fence_after();
+    for (int kb = 0; kb < p.kb; ++kb) {
+      const uint32_t sfa = tmem + SF_COL0 + sstage * SF_COLS, sfb = sfa + 4;
+      if ((kb & 3) == 0) {
+        if (!mbar_wait(smem_u32(&s.sfull[sstage]), sphase, &s.abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t src = sf + sstage * SF_BYTES;
+        cp_scales(sfa, desc_scales(src));
+        cp_scales(sfb, desc_scales(src + 512));
+        if (two) cp_scales(sfb + 4, desc_scales(src + 1024));
+      }
+      if (!mbar_wait(smem_u32(&s.full[stage]), phase, &s.abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      const uint32_t a = ring + stage * STAGE_BYTES, b = a + A_BYTES;
+      const uint32_t id = idesc | sf_id_bits(kb & 3);
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k)
+        mma_mxf8(tmem, desc_sw128(a + k * 32), desc_sw128(b + k * 32), id, sfa, sfb,
+                 (kb > 0 || k > 0) ? 1u : 0u);
+      commit(smem_u32(&s.empty[stage]));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if ((kb & 3) == 3 || kb == p.kb - 1) {
+        commit(smem_u32(&s.sempty[sstage]));
+        if (++sstage == SF_STAGES) {
+          sstage = 0;
+          sphase ^= 1u;
+        }
+      }
+    }
+    if (!ok) break;
+    commit(smem_u32(&s.tfull));
+  }
+  commit(smem_u32(&s.drain));  // all MMAs are complete before TMEM is freed
+  volatile int no_abort = 0;
+  mbar_wait(smem_u32(&s.drain), 0, &no_abort, p.status);
+}
+
+// 16-byte chunk c (0..3) of this lane's 64-byte row in the warp's staging
+// buffer, XOR-swizzled so that rows written and rows read back are free of
+// bank conflicts.
+__device__ __forceinline__ void stage_chunk(uint32_t st, int c, uint4 v) {
+  const int lane = threadIdx.x & 31;
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                   st + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// Stores the staged 32 rows x 64 bytes: `rows` rows, the first `bytes` bytes.
+__device__ __forceinline__ void flush_rows(uint32_t st, char* base, int64_t ld, int rows, int bytes) {
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(st + row * 64 + ((c ^ ((row >> 1) & 3)) << 4))
+                 : "memory");
+    if (row < rows && c * 16 < bytes)
+      *reinterpret_cast<uint4*>(base + (int64_t)row * ld + c * 16) = v;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+template <int OUT>
+__device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sync& s) {
+  const int lane = threadIdx.x & 31, ew = (threadIdx.x >> 5) - EPI_WARP0;
+  const int quarter = (threadIdx.x >> 5) & 3, half = ew >> 2;  // TMEM lanes 32 (warp mod 4) ...
+  const uint32_t st = stage_base + ew * EPI_STAGE;
+  uint32_t phase = 0;
+  const int total = total_tiles(p);
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    const Tile tl = decode_tile(p, t);
+    const int rows = min(32, tl.rows - 32 * quarter);
+    if (!warp_wait(smem_u32(&s.tfull), phase, &s.abort_flag, p.status)) return;
+    fence_after();
+    float v[128];
+    const uint32_t ta = tmem + ((uint32_t)(32 * quarter) << 16);
+    if (rows > 0) {
+      if (OUT == OUT_SITU) {
+        ld32(ta + 64 * half, v);
+        ld32(ta + 64 * half + 32, v + 32);
+        ld32(ta + SUB + 64 * half, v + 64);
+        ld32(ta + SUB + 64 * half + 32, v + 96);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ld32(ta + SUB * half + 32 * i, v + 32 * i);
+      }
+      ld_wait();
+    }
+    // the accumulator is in registers: the next tile's MMAs may start
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.tempty));
+    const int row0 = tl.m0 + 32 * quarter;
+    if (OUT == OUT_SITU) {
+      float m = 0.0f;
+      if (rows > 0) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          v[i] = situ_exact(v[i], v[64 + i], p.beta1, p.beta2);
+          m = finite_max(m, v[i]);
+        }
+      }
+      s.amax[phase][ew][lane] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.pair[quarter]));
+      if (!warp_wait(smem_u32(&s.pair[quarter]), phase, &s.abort_flag, p.status)) return;
+      if (rows > 0) {
+        m = fmaxf(m, s.amax[phase][ew ^ 4][lane]);
+        const int e = scale_exponent(m);
+        const float inv = pow2_f(-e);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float* f = v + 16 * c;
+          uint4 w;
+          w.x = pack_e4m3(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+          w.y = pack_e4m3(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+          w.z = pack_e4m3(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv);
+          w.w = pack_e4m3(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv);
+          stage_chunk(st, c, w);
+        }
+        const int col = tl.n * SUB + 64 * half;
+        flush_rows(st, static_cast<char*>(p.out) + (int64_t)row0 * p.n_out + col, p.n_out, rows,
+                   min(64, p.n_out - col));
+        if (half == 0 && lane < rows)
+          p.out_scales[((int64_t)(tl.n >> 2) * p.rows + row0 + lane) * 4 + (tl.n & 3)] =
+              (uint8_t)(e + 127);
+      }
+    } else if (rows > 0) {
+      constexpr int ES = OUT == OUT_F32 ? 4 : 2, CB = 64 / ES;  // columns of a 64-byte block
+      const int col0 = tl.n * 2 * SUB + SUB * half;
+      const int64_t ld = (int64_t)p.n_out * ES;
+      char* base = static_cast<char*>(p.out) + (int64_t)row0 * ld;
+#pragma unroll
+      for (int b = 0; b < SUB / CB; ++b) {
+        const int col = col0 + b * CB;
+        if (col < p.n_out) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float* f = v + b * CB + c * (16 / ES);
+            uint4 w;
+            if (OUT == OUT_F32)
+              w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                             __float_as_uint(f[3]));
+            else
+              w = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
+                             bf16x2(f[6], f[7]));
+            stage_chunk(st, c, w);
+          }
+          flush_rows(st, base + (int64_t)col * ES, ld, rows, min(CB, p.n_out - col) * ES);
+        }
+      }
+    }
+    phase ^= 1u;
+  }
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(THREADS, 1) experts_fp8_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Sync s;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t stage_base = ring + STAGES * STAGE_BYTES;
+  const uint32_t sf = stage_base + EPI_WARPS * EPI_STAGE;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < SF_STAGES; ++i) {
+      mbar_init(smem_u32(&s.sfull[i]), 1);
+      mbar_init(smem_u32(&s.sempty[i]), 1);
+    }
+    mbar_init(smem_u32(&s.tfull), 1);
+    mbar_init(smem_u32(&s.tempty), EPI_WARPS);
+    mbar_init(smem_u32(&s.drain), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.pair[i]), 2);
+    s.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s.tmem)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s.tmem;
+  // everything above overlaps the previous kernel; inputs are read only below
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == 0) {
+    if ((threadIdx.x & 31) == 0) produce<OUT>(p, ring, s);
+  } else if (warp == 1) {
+    if ((threadIdx.x & 31) == 0) issue_mmas<OUT>(p, ring, sf, tmem, s);
+  } else if (warp == 2) {
+    produce_scales<OUT>(p, sf, s);
+  } else {
+    epilogue<OUT>(p, tmem, stage_base, s);
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                 : "memory");
+}
+
+// ------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::mutex mu;
+  static EncodeTiledFn fn = nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  if (fn == nullptr) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  }
+  return fn;
+}
+
+// Bytes [dim2][dim1][dim0] (dim0 contiguous) with a box of 128 x rows (x 1),
+// 128-byte swizzle, zeros outside the tensor.
+bool make_map(CUtensorMap* m, const void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
+              uint32_t box_rows, uint32_t rank) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {dim0, dim1, dim2};
+  cuuint64_t strides[2] = {dim0, dim0 * dim1};
+  cuuint32_t box[3] = {(cuuint32_t)BK, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SM count of the current device, and whether a kernel's shared-memory limit
+// has been raised there.
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+struct Device {
+  int sms;
+};
+
+template <int OUT>
+cudaError_t launch(const Params& p, int64_t max_tiles, cudaStream_t st) {
+  static Device devs[kMaxDevices];
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    Device& d = devs[dev];
+    if (d.sms == 0) {
+      e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+      if (e != cudaSuccess) return e;
+      e = cudaFuncSetAttribute(experts_fp8_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               SMEM_BYTES);
+      if (e != cudaSuccess) return e;
+      d.sms = sms;
+    }
+    sms = d.sms;
+  }
+  const int grid = (int)std::min<int64_t>(max_tiles * p.n_tiles, sms);
+  if (grid <= 0) return cudaSuccess;
+  count_launch();
+  return launch_pdl(experts_fp8_kernel<OUT>, dim3(grid), dim3(THREADS), (size_t)SMEM_BYTES, st, 1,
+                    p);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st) {
+  if (g.rows == 0) return cudaSuccess;
+  Params p{};
+  bool ok = make_map(&p.tmA, g.a, g.n_in, g.rows, 1, BM, 2) &&
+            make_map(&p.tmA32, g.a, g.n_in, g.rows, 1, SMALL_ROWS, 2) &&
+            make_map(&p.tmB0, g.w, g.n_in, g.n_out, g.R, SUB, 3) &&
+            (!g.situ || make_map(&p.tmB1, g.w_up, g.n_in, g.n_out, g.R, SUB, 3));
+  if (!ok) return cudaErrorInvalidValue;
+  p.a_words = reinterpret_cast<const uint32_t*>(g.a_scales);
+  p.w_words = reinterpret_cast<const uint32_t*>(g.w_scales);
+  p.w_up_words = reinterpret_cast<const uint32_t*>(g.w_up_scales);
+  p.rows = (int)g.rows;
+  p.words = q_words(g.n_in);
+  p.w_blocks = q_blocks(g.n_out);
+  p.kb = q_blocks(g.n_in);
+  p.n_out = g.n_out;
+  p.tiles = g.tiles;
+  p.n_mtiles = g.n_mtiles;
+  p.out = g.out;
+  p.out_scales = g.out_scales;
+  p.status = status;
+  p.beta1 = g.beta1;
+  p.beta2 = g.beta2;
+  p.n_tiles = g.situ ? p.w_blocks : (g.n_out + 2 * SUB - 1) / (2 * SUB);
+  const int64_t max_tiles = g.tiles != nullptr ? g.max_tiles : (g.rows + BM - 1) / BM;
+  if (g.situ) return launch<OUT_SITU>(p, max_tiles, st);
+  return g.out_f32 ? launch<OUT_F32>(p, max_tiles, st) : launch<OUT_BF16>(p, max_tiles, st);
+}
+
+}  // namespace lmoe

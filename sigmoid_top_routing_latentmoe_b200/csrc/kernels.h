@@ -19,6 +19,22 @@ cudaError_t launch_route_gemv(const T* x, const T* w_r, const float* bias, int64
 cudaError_t launch_route_topk(const float* logits, int64_t ld, const float* bias, int64_t n, int R,
                               int k, int router, int32_t* ids, float* probs, cudaStream_t st);
 
+// Routing of given logits under a rule with groups of experts (route_rule.cu).
+struct RouteRule {
+  int softmax;       // scores: 0 sigmoid, 1 softmax over all experts
+  int n_groups, topk_groups;
+  int top2;          // a group's score: 1 the sum of its two largest keys, 0 the largest
+  int renormalise;
+  float scale;
+};
+cudaError_t launch_route_rule(const RouteRule& rule, const float* logits, int64_t ld,
+                              const float* bias, int64_t n, int R, int k, int32_t* ids,
+                              float* probs, cudaStream_t st);
+// dlogits [n, R] (row stride ldd) of <dprobs, probs>.
+cudaError_t launch_route_rule_backward(const RouteRule& rule, const float* logits, int64_t ld,
+                                       const int32_t* ids, const float* dprobs, int64_t n, int R,
+                                       int k, float* dlogits, int64_t ldd, cudaStream_t st);
+
 // ------------------------------------------------------ router balancing losses
 // Blocks of this many tokens each leave fixed-order partial sums.
 constexpr int kLossRows = 256;

@@ -1,0 +1,238 @@
+// Quantisers to e4m3 with one power-of-two scale (E8M0) for each block of 128
+// columns of a row, or each 128 x 128 block of a weight matrix.
+//
+// With amax the largest finite magnitude of a block, the scale is 2^e with the
+// smallest e >= -126 such that amax <= 448 * 2^e (448: the largest e4m3
+// value); q = round-to-nearest-even e4m3 of x * 2^-e.  The division is exact,
+// so each element is rounded once.  The scale is stored as the byte e + 127; a
+// block of zeros has scale 1.  A NaN or an infinity becomes NaN: 8 bits hold
+// no infinity, and a clamped one would hide an overflow.
+//
+// Both kernels are bound by memory: they read each element once (16-byte
+// loads) and keep it in registers between the maximum and the rounding.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "experts_fp8.h"
+#include "kernels.h"
+#include "launch.h"
+#include "quantize.cuh"
+
+namespace lmoe {
+namespace {
+
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);  // elements of a 16-byte vector
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[kVec<T>]);
+template <>
+__device__ __forceinline__ void unpack<float>(const uint4& v, float (&f)[4]) {
+  f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+  f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+}
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <typename T>
+__device__ __forceinline__ float vec_amax(const uint4& v) {
+  float f[kVec<T>];
+  unpack<T>(v, f);
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) m = finite_max(m, f[i]);
+  return m;
+}
+// Quantises the vector's elements and stores them at q (4 or 8 bytes).
+template <typename T>
+__device__ __forceinline__ void store_q(uint8_t* q, const uint4& v, float inv) {
+  float f[kVec<T>];
+  unpack<T>(v, f);
+  uint32_t w[kVec<T> / 4];
+#pragma unroll
+  for (int i = 0; i < kVec<T> / 4; ++i)
+    w[i] = pack_e4m3(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv, f[4 * i + 3] * inv);
+  if constexpr (kVec<T> == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(q) = w[0];
+}
+
+// One warp per row.  A block's 128 elements lie in kBlockLanes lanes (16 for
+// bf16, 32 for fp32), so one warp-wide load covers 2 or 1 blocks; U loads are
+// in flight before the first maximum.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ x, int64_t n_src,
+                                                            int64_t ld,
+                                                            const int32_t* __restrict__ index,
+                                                            int64_t rows, int cols,
+                                                            uint8_t* __restrict__ q,
+                                                            uint8_t* __restrict__ scales) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int V = kVec<T>, BL = kQBlock / V, U = 4;
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  int64_t src = r;
+  bool have = true;
+  if (index != nullptr) {
+    src = index[r];
+    have = src >= 0 && src < n_src;
+  }
+  const uint4* xr = reinterpret_cast<const uint4*>(x + (have ? src : 0) * ld);
+  const int nvec = cols / V;
+  const int blocks = (cols + kQBlock - 1) / kQBlock, blocks4 = (blocks + 3) & ~3;
+  for (int v0 = 0; v0 * V < blocks4 * kQBlock; v0 += 32 * U) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = v0 + u * 32 + lane;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (have && at < nvec) v[u] = xr[at];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = v0 + u * 32 + lane;
+      float m = vec_amax<T>(v[u]);
+#pragma unroll
+      for (int off = BL / 2; off > 0; off >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      const int e = scale_exponent(m);
+      if (at < nvec) store_q<T>(q + r * cols + (int64_t)at * V, v[u], pow2_f(-e));
+      const int b = at / BL;
+      if (lane % BL == 0 && b < blocks4)
+        scales[((int64_t)(b >> 2) * rows + r) * 4 + (b & 3)] = (uint8_t)(e + 127);
+    }
+  }
+}
+
+// One thread block per 128 x 128 block (or per block of padding bytes).
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_weights_kernel(const T* __restrict__ w,
+                                                               int64_t rows, int cols, int rb,
+                                                               int cb4, uint8_t* __restrict__ q,
+                                                               uint8_t* __restrict__ scales) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int V = kVec<T>, BL = kQBlock / V, RP = 256 / BL, U = kQBlock / RP;
+  __shared__ float part[8];
+  const int64_t blk = blockIdx.x;
+  const int cbi = (int)(blk % cb4);
+  const int rbi = (int)((blk / cb4) % rb);
+  const int64_t mat = blk / ((int64_t)cb4 * rb);
+  const int c = cbi * kQBlock + (threadIdx.x % BL) * V;
+  const int64_t r0 = (int64_t)rbi * kQBlock + threadIdx.x / BL;
+  uint4 v[U];
+  float m = 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    v[u] = make_uint4(0, 0, 0, 0);
+    const int64_t r = r0 + u * RP;
+    if (c < cols && r < rows)
+      v[u] = *reinterpret_cast<const uint4*>(w + (mat * rows + r) * cols + c);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) m = fmaxf(m, vec_amax<T>(v[u]));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
+  const int e = scale_exponent(m);
+  const float inv = pow2_f(-e);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t r = r0 + u * RP;
+    if (c < cols && r < rows) store_q<T>(q + (mat * rows + r) * cols + c, v[u], inv);
+  }
+  if (threadIdx.x == 0) scales[blk] = (uint8_t)(e + 127);
+}
+
+// The tile list of a ragged product: expert e's rows [offsets[e], offsets[e + 1])
+// in tiles of at most kTileM.  Offsets are clamped to an ascending order inside
+// [0, rows] and the list to max_tiles, so that no list leads a product out of
+// its buffers.  One block; a block-wide scan over 1024 experts at a time.
+__global__ void __launch_bounds__(1024) expert_tiles_kernel(TileList t) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ int warp_sum[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int base = 0;
+  for (int e0 = 0; e0 < t.R; e0 += 1024) {
+    const int e = e0 + threadIdx.x;
+    int lo = 0, hi = 0;
+    if (e < t.R) {
+      lo = (int)min((int64_t)max(t.offsets[e], 0), t.rows);
+      hi = (int)min((int64_t)max(t.offsets[e + 1], lo), t.rows);
+    }
+    const int n = (hi - lo + kTileM - 1) / kTileM;
+    int inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int s = warp_sum[w];
+      if (w < warp) before += s;
+      total += s;
+    }
+    int at = base + before + inc - n;
+    for (int j = 0; j < n; ++j, ++at)
+      if (at < t.max_tiles)
+        t.tiles[at] = make_int4(e, lo + j * kTileM, min(kTileM, hi - lo - j * kTileM), 0);
+    base += total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *t.n_mtiles = min(base, t.max_tiles);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_quantize_rows(const T* x, int64_t n_src, int64_t ld, const int32_t* index,
+                                 int64_t rows, int cols, uint8_t* q, uint8_t* scales,
+                                 cudaStream_t st) {
+  if (rows == 0) return cudaSuccess;
+  const int warps = 8;
+  count_launch();
+  return launch_pdl(quantize_rows_kernel<T>, dim3((unsigned)((rows + warps - 1) / warps)),
+                    dim3(warps * 32), 0, st, 1, x, n_src, ld, index, rows, cols, q, scales);
+}
+template cudaError_t launch_quantize_rows<float>(const float*, int64_t, int64_t, const int32_t*,
+                                                 int64_t, int, uint8_t*, uint8_t*, cudaStream_t);
+template cudaError_t launch_quantize_rows<__nv_bfloat16>(const __nv_bfloat16*, int64_t, int64_t,
+                                                         const int32_t*, int64_t, int, uint8_t*,
+                                                         uint8_t*, cudaStream_t);
+
+template <typename T>
+cudaError_t launch_quantize_weights(const T* w, int64_t mats, int64_t rows, int cols, uint8_t* q,
+                                    uint8_t* scales, cudaStream_t st) {
+  if (mats == 0) return cudaSuccess;
+  const int rb = q_blocks(rows), cb4 = 4 * q_words(cols);
+  count_launch();
+  return launch_pdl(quantize_weights_kernel<T>, dim3((unsigned)(mats * rb * cb4)), dim3(256), 0, st,
+                    1, w, rows, cols, rb, cb4, q, scales);
+}
+template cudaError_t launch_quantize_weights<float>(const float*, int64_t, int64_t, int, uint8_t*,
+                                                    uint8_t*, cudaStream_t);
+template cudaError_t launch_quantize_weights<__nv_bfloat16>(const __nv_bfloat16*, int64_t, int64_t,
+                                                            int, uint8_t*, uint8_t*, cudaStream_t);
+
+cudaError_t launch_expert_tiles(const TileList& t, cudaStream_t st) {
+  count_launch();
+  return launch_pdl(expert_tiles_kernel, dim3(1), dim3(1024), 0, st, 1, t);
+}
+
+}  // namespace lmoe
