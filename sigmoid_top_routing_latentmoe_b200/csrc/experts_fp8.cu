@@ -260,6 +260,67 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// ------------------------------------------------------------- hidden units
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// tanh(x) / x as polynomials in u = x^2, fitted by least squares with the
+// weights moved towards the largest relative error: relative error in 32 bits
+// at most 4.2 * 2^-24 for |x| <= kGateX, 1.9 * 2^-24 for |x| <= kUpX.
+constexpr float kGateX = 1.5f, kUpX = 0.5f;
+__device__ __forceinline__ float gate_poly(float u) {
+  float p = 2.553440027e-05f;
+  p = fmaf(p, u, -3.205151297e-04f);
+  p = fmaf(p, u, 1.872322173e-03f);
+  p = fmaf(p, u, -7.067439146e-03f);
+  p = fmaf(p, u, 2.066442743e-02f);
+  p = fmaf(p, u, -5.348970741e-02f);
+  p = fmaf(p, u, 1.332349330e-01f);
+  p = fmaf(p, u, -3.333253562e-01f);
+  return fmaf(p, u, 9.999998808e-01f);
+}
+__device__ __forceinline__ float up_poly(float u) {
+  float p = 1.713500172e-02f;
+  p = fmaf(p, u, -5.298607424e-02f);
+  p = fmaf(p, u, 1.332477927e-01f);
+  p = fmaf(p, u, -3.333306909e-01f);
+  return fmaf(p, u, 1.0f);
+}
+// SiTU-GLU hidden unit beta1 tanh(a / beta1) sigmoid(a) beta2 tanh(c / beta2)
+// to a few 2^-24 of its value: the hidden unit is rounded to e4m3 next, and a
+// coarser value would fall on the other side of a rounding border more often.
+// Near zero, tanh(x) = x P(x^2): no cancellation, and beta tanh(a / beta) =
+// a P.  Beyond (WIDE; |x| > kGateX, kUpX), tanh(x) = (1 - t) / (1 + t) with
+// t = e^(-2 |x|), its denominator shared with the sigmoid's.
+template <bool WIDE>
+__device__ __forceinline__ float situ_unit(float a, float c, float b1, float b2, float i1, float i2) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float x1 = a * i1, x2 = c * i2;
+  float n1 = a * gate_poly(x1 * x1), n2 = c * up_poly(x2 * x2);
+  float d = 1.0f + ex2(-kLog2e * a);
+  if (WIDE) {
+    const float t1 = ex2(-2.0f * kLog2e * fabsf(x1)), t2 = ex2(-2.0f * kLog2e * fabsf(x2));
+    float e1 = 1.0f, e2 = 1.0f;
+    if (fabsf(x1) > kGateX) {
+      n1 = copysignf(b1 - b1 * t1, a);
+      e1 = 1.0f + t1;
+    }
+    if (fabsf(x2) > kUpX) {
+      n2 = copysignf(b2 - b2 * t2, c);
+      e2 = 1.0f + t2;
+    }
+    d *= e1 * e2;
+  }
+  return n1 * n2 * rcp(d);
+}
+
 template <int OUT>
 __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sync& s) {
   const int lane = threadIdx.x & 31, ew = (threadIdx.x >> 5) - EPI_WARP0;
@@ -294,11 +355,24 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
     if (OUT == OUT_SITU) {
       float m = 0.0f;
       if (rows > 0) {
+        float ma = 0.0f, mc = 0.0f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          v[i] = situ_exact(v[i], v[64 + i], p.beta1, p.beta2);
-          m = finite_max(m, v[i]);
+          ma = fmaxf(ma, fabsf(v[i]));
+          mc = fmaxf(mc, fabsf(v[64 + i]));
         }
+        const float i1 = 1.0f / p.beta1, i2 = 1.0f / p.beta2;
+        if (__any_sync(0xffffffffu, ma * i1 > kGateX || mc * i2 > kUpX)) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            v[i] = situ_unit<true>(v[i], v[64 + i], p.beta1, p.beta2, i1, i2);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            v[i] = situ_unit<false>(v[i], v[64 + i], p.beta1, p.beta2, i1, i2);
+        }
+#pragma unroll
+        for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(v[i]));  // finite, or NaN: left out
       }
       s.amax[phase][ew][lane] = m;
       __syncwarp();
@@ -312,10 +386,10 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
         for (int c = 0; c < 4; ++c) {
           const float* f = v + 16 * c;
           uint4 w;
-          w.x = pack_e4m3(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-          w.y = pack_e4m3(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-          w.z = pack_e4m3(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv);
-          w.w = pack_e4m3(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv);
+          w.x = pack_e4m3_finite(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+          w.y = pack_e4m3_finite(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+          w.z = pack_e4m3_finite(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv);
+          w.w = pack_e4m3_finite(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv);
           stage_chunk(st, c, w);
         }
         const int col = tl.n * SUB + 64 * half;

@@ -25,14 +25,16 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 __device__ __forceinline__ float pow2_f(int e) {  // -126 <= e <= 127
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
+// Four e4m3 values of finite numbers or NaN, the first in the lowest byte.
+__device__ __forceinline__ uint32_t pack_e4m3_finite(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
 // Four e4m3 values, the first in the lowest byte; NaN and infinities give NaN.
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
   const float z = 0.0f;  // x + (x * 0): NaN for an infinity, x otherwise
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-      make_float2(a + a * z, b + b * z), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-      make_float2(c + c * z, d + d * z), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+  return pack_e4m3_finite(a + a * z, b + b * z, c + c * z, d + d * z);
 }
 
 }  // namespace lmoe
