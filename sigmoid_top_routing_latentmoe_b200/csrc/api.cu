@@ -327,11 +327,11 @@ static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* of
   return t;
 }
 
-// Rows of z quantised in sorted order, gate and up products with the SiTU and
-// the quantisation of the hidden units in their epilogue, output product.  The
-// quantised rows take the first half of the workspace's sorted-row area (which
-// holds rows of 2 or 4 bytes an element) and their scales the second; the
-// hidden units likewise.
+// The rows of z quantised once, gate and up products (which gather each pair's
+// row) with the SiTU and the quantisation of the hidden units in their
+// epilogue, output product.  The quantised rows take the first half of the
+// workspace's sorted-row area (rows of 2 or 4 bytes an element) and their scales the
+// second; the hidden units likewise theirs.
 template <typename T>
 static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const int32_t* perm,
                                       const int32_t* offsets, const lmoe_fp8_experts* w, void* out,
@@ -341,7 +341,7 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   if (P == 0) return LMOE_OK;
   const int Lt = d->latent, F = d->ff_routed;
   uint8_t* zq = at<uint8_t>(ws, L.zp);
-  uint8_t* zs = zq + P * Lt;
+  uint8_t* zs = zq + d->n_tokens * Lt;
   uint8_t* hq = at<uint8_t>(ws, L.h);
   uint8_t* hs = hq + P * F;
   const TileList tl = tile_list(d, L, offsets, ws);
@@ -349,7 +349,8 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   {
     ProfScope ps("quantize", st);
     LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");
-    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, perm, P, Lt, zq, zs, st),
+    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, nullptr, d->n_tokens, Lt, zq,
+                                      zs, st),
               "quantize rows");
   }
   Fp8Gemm g{};
@@ -357,7 +358,7 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   g.max_tiles = tl.max_tiles; g.beta1 = d->beta1; g.beta2 = d->beta2;
   {
     ProfScope ps("expert_gemm1", st);
-    g.a = zq; g.a_scales = zs; g.n_in = Lt; g.n_out = F; g.situ = 1;
+    g.a = zq; g.a_scales = zs; g.a_rows = d->n_tokens; g.index = perm; g.n_in = Lt; g.n_out = F; g.situ = 1;
     g.w = (const uint8_t*)w->w_g; g.w_scales = w->w_g_scales;
     g.w_up = (const uint8_t*)w->w_u; g.w_up_scales = w->w_u_scales;
     g.out = hq; g.out_scales = hs;
@@ -365,7 +366,7 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   }
   {
     ProfScope ps("expert_gemm2", st);
-    g.a = hq; g.a_scales = hs; g.n_in = F; g.n_out = Lt; g.situ = 0;
+    g.a = hq; g.a_scales = hs; g.a_rows = P; g.index = nullptr; g.n_in = F; g.n_out = Lt; g.situ = 0;
     g.w = (const uint8_t*)w->w_o; g.w_scales = w->w_o_scales;
     g.out = out; g.out_f32 = std::is_same<T, float>::value ? 1 : 0;
     LMOE_CUDA(launch_fp8_gemm(g, status, st), "routed gemm2 (8-bit)");
@@ -1090,7 +1091,7 @@ lmoe_status moe_expert_gemm_fp8(const lmoe_dims* dims, int32_t n_in, int32_t n_o
   const Layout L = layout(dims, false);
   const TileList tl = tile_list(dims, L, offsets, ws);
   Fp8Gemm g{};
-  g.a = (const uint8_t*)a; g.a_scales = a_scales; g.rows = tl.rows; g.R = dims->n_routed;
+  g.a = (const uint8_t*)a; g.a_scales = a_scales; g.a_rows = g.rows = tl.rows; g.R = dims->n_routed;
   g.n_in = n_in; g.n_out = n_out; g.w = (const uint8_t*)w; g.w_scales = w_scales; g.out = out;
   g.out_f32 = dims->dtype == LMOE_F32 ? 1 : 0;
   if (offsets != nullptr) {

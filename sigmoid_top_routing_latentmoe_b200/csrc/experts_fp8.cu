@@ -13,7 +13,8 @@
 //              copies the next four blocks' scale words to TMEM,
 //   warp 2     scale producer: the words of four K blocks (128 rows of A, one
 //              or two weight blocks) in the order tcgen05.cp wants,
-//   warps 3-10 epilogue, two per 32-row quarter, each taking half the columns.
+//   warps 4-11 epilogue, two per 32-row quarter, each taking half the columns,
+//   warps 12-15  SiTU: copy the rows of A that p.index names.
 #include <cuda.h>
 
 #include <algorithm>
@@ -38,8 +39,14 @@ constexpr int SMALL_ROWS = 32;            // tiles of at most this many rows loa
 constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
 constexpr int SF_BYTES = 3 * 512;         // A words, then two blocks of B words
 constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
-constexpr int EPI_WARPS = 8, EPI_WARP0 = 3, EPI_STAGE = 32 * 64;  // 32 rows x 64 bytes per warp
-constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, EPI_STAGE = 32 * 64;  // 32 rows x 64 bytes per warp
+constexpr int GATHER_WARPS = 4;
+template <int OUT>
+constexpr int kThreads = 32 * (EPI_WARP0 + EPI_WARPS + (OUT == 2 ? GATHER_WARPS : 0));
+// The SiTU kernel's 512 threads start with 128 registers each; its 8 epilogue
+// warps hold 128 accumulators a thread and take what the others give up
+// (2 warpgroups x 176 + 2 x 80 = 4 x 128).
+constexpr int REGS_EPI = 176, REGS_OTHER = 80;
 constexpr int SMEM_BYTES =
     STAGES * STAGE_BYTES + EPI_WARPS * EPI_STAGE + SF_STAGES * SF_BYTES + 1024;
 constexpr int TMEM_COLS = 512, SF_COL0 = 256;
@@ -50,9 +57,12 @@ enum Out { OUT_BF16 = 0, OUT_F32 = 1, OUT_SITU = 2 };
 
 struct Params {
   CUtensorMap tmA, tmA32, tmB0, tmB1;
-  const uint32_t* a_words;               // [words, rows]
+  const uint8_t* a;                      // with index
+  const uint32_t* a_words;               // [words, a_rows]
+  const int32_t* index;
+  int a_rows;
   const uint32_t *w_words, *w_up_words;  // [R, w_blocks, words]
-  int rows, words, w_blocks, kb, n_tiles, n_out;
+  int rows, words, w_blocks, kb, n_tiles, n_in, n_out;
   const int4* tiles;
   const int32_t* n_mtiles;
   void* out;
@@ -87,8 +97,11 @@ struct Sync {
   volatile int abort_flag;
 };
 
+// The SiTU product takes its rows of A through p.index (gather_rows), the
+// others their neighbouring rows by TMA.
 template <int OUT>
 __device__ void produce(const Params& p, uint32_t ring, Sync& s) {
+  constexpr bool GATHER = OUT == OUT_SITU;
   int stage = 0;
   uint32_t phase = 0, issued = 0, issued_phase = 0;
   bool ok = true;
@@ -101,7 +114,7 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s) {
     const int row0 = OUT == OUT_SITU ? tl.n * SUB : tl.n * 2 * SUB;
     const int row1 = OUT == OUT_SITU ? row0 : row0 + SUB;
     const uint32_t bytes =
-        (small ? SMALL_ROWS * BK : A_BYTES) + (two ? B_BYTES : B_BYTES / 2);
+        (GATHER ? 0 : small ? SMALL_ROWS * BK : A_BYTES) + (two ? B_BYTES : B_BYTES / 2);
     for (int kb = 0; kb < p.kb; ++kb) {
       if (!mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, &s.abort_flag, p.status)) {
         ok = false;
@@ -109,7 +122,7 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s) {
       }
       const uint32_t dst = ring + stage * STAGE_BYTES, bar = smem_u32(&s.full[stage]);
       mbar_expect_tx(bar, bytes);
-      tma_load_2d(dst, map_a, bar, kb * BK, tl.m0);
+      if (!GATHER) tma_load_2d(dst, map_a, bar, kb * BK, tl.m0);
       tma_load_3d(dst + A_BYTES, &p.tmB0, bar, kb * BK, row0, tl.e);
       if (two) tma_load_3d(dst + A_BYTES + SUB * BK, map_b1, bar, kb * BK, row1, tl.e);
       issued |= 1u << stage;
@@ -120,12 +133,88 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s) {
       }
     }
   }
-  // every load issued has landed before the block exits
+  // every load issued has landed before the block exits (a stage's barrier may
+  // still lack the gather warp's arrival after an abort: then the cap ends the wait)
   for (int i = 0; i < STAGES; ++i)
     if (issued & (1u << i)) {
       volatile int no_abort = 0;
       mbar_wait(smem_u32(&s.full[i]), (issued_phase >> i) & 1u, &no_abort, p.status);
     }
+}
+
+// Rows of A by index, four warps with 32 rows each, by 16-byte asynchronous
+// copies into the swizzled layout a TMA load would leave.  A stage is
+// announced once its copies have landed; up to IN_FLIGHT stages stay in
+// flight, but none while the ring is full, when the tensor cores may be
+// waiting for exactly these.
+constexpr int IN_FLIGHT = 2;
+__device__ __forceinline__ void load_index(const Params& p, const Tile& tl, int row0, int (&row)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = row0 + 4 * i;
+    row[i] = r < tl.rows ? p.index[tl.m0 + r] : -1;
+  }
+}
+__device__ void gather_rows(const Params& p, uint32_t ring, Sync& s) {
+  const int lane = threadIdx.x & 31;
+  const int chunk = lane & 7, row0 = 32 * ((threadIdx.x >> 5) & 3) + (lane >> 3);
+  int stage = 0, head = 0;  // next stage to fill, oldest stage in flight
+  int flying = 0;
+  uint32_t phase = 0;
+  const int total = total_tiles(p);
+  auto announce = [&](int n) {  // the n oldest stages have landed
+    fence_async_smem();
+    __syncwarp();
+    for (int i = 0; i < n; ++i) {
+      if (lane == 0) mbar_arrive(smem_u32(&s.full[head]));
+      if (++head == STAGES) head = 0;
+    }
+    flying -= n;
+  };
+  int row[8], next[8];
+  Tile tl{0, 0, 0, 0};
+  if ((int)blockIdx.x < total) tl = decode_tile(p, blockIdx.x);
+  load_index(p, tl, row0, row);
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    Tile tn{0, 0, 0, 0};
+    if (t + (int)gridDim.x < total) tn = decode_tile(p, t + gridDim.x);
+    load_index(p, tn, row0, next);
+    for (int kb = 0; kb < p.kb; ++kb) {
+      const uint32_t empty = smem_u32(&s.empty[stage]);
+      if (flying > 0 && !__all_sync(0xffffffffu, mbar_try_wait(empty, phase ^ 1u))) {
+        cp_async_wait<0>();
+        announce(flying);
+      }
+      if (!warp_wait(empty, phase ^ 1u, &s.abort_flag, p.status)) {
+        cp_async_wait<0>();
+        return;
+      }
+      const uint32_t dst = ring + stage * STAGE_BYTES;
+      const int col = kb * BK + chunk * 16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = row0 + 4 * i;
+        const bool have = col < p.n_in && (uint32_t)row[i] < (uint32_t)p.a_rows;
+        const uint8_t* src = p.a + (have ? (int64_t)row[i] * p.n_in + col : 0);
+        cp_async16(dst + r * BK + ((chunk ^ (r & 7)) << 4), src, have ? 16 : 0);
+      }
+      cp_async_commit();
+      ++flying;
+      if (flying > IN_FLIGHT) {
+        cp_async_wait<IN_FLIGHT>();
+        announce(flying - IN_FLIGHT);
+      }
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) row[i] = next[i];
+    tl = tn;
+  }
+  cp_async_wait<0>();
+  announce(flying);
 }
 
 // Scale words of four K blocks: row r of A at byte (r % 32) * 16 + (r / 32) * 4,
@@ -144,13 +233,18 @@ __device__ void produce_scales(const Params& p, uint32_t sf, Sync& s) {
     const uint32_t* w0 = p.w_words + ((int64_t)tl.e * p.w_blocks + nb0) * p.words;
     const uint32_t* w1 =
         OUT == OUT_SITU ? p.w_up_words + ((int64_t)tl.e * p.w_blocks + nb0) * p.words : w0 + p.words;
+    int row[4];  // rows of A, -1: none (its product is not stored, or of zeros)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = lane + 32 * j;
+      row[j] = r >= tl.rows ? -1 : OUT == OUT_SITU ? p.index[tl.m0 + r] : tl.m0 + r;
+      if (row[j] >= p.a_rows) row[j] = -1;
+    }
     for (int q = 0; q < p.words; ++q) {
       uint32_t a[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = lane + 32 * j;  // words of rows past the tile scale rows never stored
-        a[j] = r < tl.rows ? p.a_words[(int64_t)q * p.rows + tl.m0 + r] : 0u;
-      }
+      for (int j = 0; j < 4; ++j)
+        a[j] = row[j] >= 0 ? p.a_words[(int64_t)q * p.a_rows + row[j]] : 0u;
       const uint32_t b0 = w0[q], b1 = two ? w1[q] : 0u;
       if (!warp_wait(smem_u32(&s.sempty[stage]), phase ^ 1u, &s.abort_flag, p.status)) return;
       const uint32_t dst = sf + stage * SF_BYTES + lane * 16;
@@ -429,7 +523,7 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
 }
 
 template <int OUT>
-__global__ void __launch_bounds__(THREADS, 1) experts_fp8_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads<OUT>, 1) experts_fp8_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync s;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -438,7 +532,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_fp8_kernel(const __grid_co
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.full[i]), OUT == OUT_SITU ? 1 + GATHER_WARPS : 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < SF_STAGES; ++i) {
@@ -467,14 +561,21 @@ __global__ void __launch_bounds__(THREADS, 1) experts_fp8_kernel(const __grid_co
   pdl_trigger();
   pdl_wait();
 
-  if (warp == 0) {
-    if ((threadIdx.x & 31) == 0) produce<OUT>(p, ring, s);
-  } else if (warp == 1) {
-    if ((threadIdx.x & 31) == 0) issue_mmas<OUT>(p, ring, sf, tmem, s);
-  } else if (warp == 2) {
-    produce_scales<OUT>(p, sf, s);
-  } else {
+  if (warp < EPI_WARP0) {
+    if (OUT == OUT_SITU) regs_dec<REGS_OTHER>();
+    if (warp == 0) {
+      if ((threadIdx.x & 31) == 0) produce<OUT>(p, ring, s);
+    } else if (warp == 1) {
+      if ((threadIdx.x & 31) == 0) issue_mmas<OUT>(p, ring, sf, tmem, s);
+    } else if (warp == 2) {
+      produce_scales<OUT>(p, sf, s);
+    }
+  } else if (warp < EPI_WARP0 + EPI_WARPS) {
+    if (OUT == OUT_SITU) regs_inc<REGS_EPI>();
     epilogue<OUT>(p, tmem, stage_base, s);
+  } else if (OUT == OUT_SITU) {
+    regs_dec<REGS_OTHER>();
+    gather_rows(p, ring, s);
   }
 
   fence_before();
@@ -552,7 +653,7 @@ cudaError_t launch(const Params& p, int64_t max_tiles, cudaStream_t st) {
   const int grid = (int)std::min<int64_t>(max_tiles * p.n_tiles, sms);
   if (grid <= 0) return cudaSuccess;
   count_launch();
-  return launch_pdl(experts_fp8_kernel<OUT>, dim3(grid), dim3(THREADS), (size_t)SMEM_BYTES, st, 1,
+  return launch_pdl(experts_fp8_kernel<OUT>, dim3(grid), dim3(kThreads<OUT>), (size_t)SMEM_BYTES, st, 1,
                     p);
 }
 
@@ -561,14 +662,19 @@ cudaError_t launch(const Params& p, int64_t max_tiles, cudaStream_t st) {
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st) {
   if (g.rows == 0) return cudaSuccess;
   Params p{};
-  bool ok = make_map(&p.tmA, g.a, g.n_in, g.rows, 1, BM, 2) &&
-            make_map(&p.tmA32, g.a, g.n_in, g.rows, 1, SMALL_ROWS, 2) &&
+  if (g.situ != (g.index != nullptr)) return cudaErrorInvalidValue;
+  bool ok = (g.situ || (make_map(&p.tmA, g.a, g.n_in, g.a_rows, 1, BM, 2) &&
+                        make_map(&p.tmA32, g.a, g.n_in, g.a_rows, 1, SMALL_ROWS, 2))) &&
             make_map(&p.tmB0, g.w, g.n_in, g.n_out, g.R, SUB, 3) &&
             (!g.situ || make_map(&p.tmB1, g.w_up, g.n_in, g.n_out, g.R, SUB, 3));
   if (!ok) return cudaErrorInvalidValue;
   p.a_words = reinterpret_cast<const uint32_t*>(g.a_scales);
   p.w_words = reinterpret_cast<const uint32_t*>(g.w_scales);
   p.w_up_words = reinterpret_cast<const uint32_t*>(g.w_up_scales);
+  p.a = g.a;
+  p.n_in = g.n_in;
+  p.index = g.index;
+  p.a_rows = (int)g.a_rows;
   p.rows = (int)g.rows;
   p.words = q_words(g.n_in);
   p.w_blocks = q_blocks(g.n_out);
