@@ -13,8 +13,8 @@
 //              copies the next four blocks' scale words to TMEM,
 //   warp 2     scale producer: the words of four K blocks (128 rows of A, one
 //              or two weight blocks) in the order tcgen05.cp wants,
-//   warps 4-11 epilogue, two per 32-row quarter, each taking half the columns,
-//   warps 12-15  SiTU: copy the rows of A that p.index names.
+//   warps 4-   epilogue, two (SiTU: four) per 32-row quarter, sharing its columns,
+//   then, SiTU only, four warps that copy the rows of A that p.index names.
 #include <cuda.h>
 
 #include <algorithm>
@@ -39,21 +39,29 @@ constexpr int SMALL_ROWS = 32;            // tiles of at most this many rows loa
 constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
 constexpr int SF_BYTES = 3 * 512;         // A words, then two blocks of B words
 constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
-constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, EPI_STAGE = 32 * 64;  // 32 rows x 64 bytes per warp
-constexpr int GATHER_WARPS = 4;
+constexpr int EPI_WARP0 = 4;
+enum Out { OUT_BF16 = 0, OUT_F32 = 1, OUT_SITU = 2 };
+// Epilogue warps share a 32-row quarter of the tile by columns.  Plain tiles: 2
+// warps with 128 columns each; SiTU tiles: 4 warps with 32 hidden units each,
+// whose 64 accumulators leave the compiler room to overlap the units (with 2
+// warps and 128 accumulators the mid layer's product took 426 us).
 template <int OUT>
-constexpr int kThreads = 32 * (EPI_WARP0 + EPI_WARPS + (OUT == 2 ? GATHER_WARPS : 0));
-// The SiTU kernel's 512 threads start with 128 registers each; its 8 epilogue
-// warps hold 128 accumulators a thread and take what the others give up
-// (2 warpgroups x 176 + 2 x 80 = 4 x 128).
-constexpr int REGS_EPI = 176, REGS_OTHER = 80;
-constexpr int SMEM_BYTES =
-    STAGES * STAGE_BYTES + EPI_WARPS * EPI_STAGE + SF_STAGES * SF_BYTES + 1024;
+struct Cfg {
+  static constexpr int SPLIT = OUT == OUT_SITU ? 4 : 2;   // warps per quarter
+  static constexpr int EPI_WARPS = 4 * SPLIT;
+  static constexpr int GATHER_WARP0 = EPI_WARP0 + EPI_WARPS;
+  static constexpr int GATHER_WARPS = OUT == OUT_SITU ? 4 : 0;
+  static constexpr int THREADS = 32 * (GATHER_WARP0 + GATHER_WARPS);
+  static constexpr int EPI_STAGE = 32 * (OUT == OUT_SITU ? 32 : 64);  // bytes per warp
+};
+constexpr int EPI_BYTES = 8 * 32 * 64;    // staging of all epilogue warps
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + SF_STAGES * SF_BYTES + 1024;
+// The SiTU kernel's 768 threads start with 80 registers each; its 16 epilogue
+// warps take what the other 8 give up (512 x 96 + 256 x 48 = 768 x 80).
+constexpr int REGS_EPI = 96, REGS_OTHER = 48;
 constexpr int TMEM_COLS = 512, SF_COL0 = 256;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 static_assert(SF_COL0 + SF_STAGES * SF_COLS <= TMEM_COLS, "TMEM");
-
-enum Out { OUT_BF16 = 0, OUT_F32 = 1, OUT_SITU = 2 };
 
 struct Params {
   CUtensorMap tmA, tmA32, tmB0, tmB1;
@@ -91,8 +99,8 @@ __device__ __forceinline__ bool two_subs(const Params& p, const Tile& tl) {
 
 struct Sync {
   uint64_t full[STAGES], empty[STAGES], sfull[SF_STAGES], sempty[SF_STAGES], tfull, tempty, drain,
-      pair[4];
-  float amax[2][EPI_WARPS][32];
+      quarter[4];
+  float amax[2][4][4][32];  // tile parity, quarter, warp of the quarter, row
   uint32_t tmem;
   volatile int abort_flag;
 };
@@ -146,75 +154,76 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s) {
 // copies into the swizzled layout a TMA load would leave.  A stage is
 // announced once its copies have landed; up to IN_FLIGHT stages stay in
 // flight, but none while the ring is full, when the tensor cores may be
-// waiting for exactly these.
+// waiting for exactly these.  Every copy reads inside its row, so that none
+// needs zero-filling (whose branches took four times as long): columns past
+// n_in repeat the last ones (they meet zeros of W), rows past the tile repeat
+// its last row (never stored), and an index outside A reads row 0 (its scale
+// words are 0, and so is its product).
 constexpr int IN_FLIGHT = 2;
 __device__ __forceinline__ void load_index(const Params& p, const Tile& tl, int row0, int (&row)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int r = row0 + 4 * i;
-    row[i] = r < tl.rows ? p.index[tl.m0 + r] : -1;
+    const int r = min(row0 + 4 * i, tl.rows - 1);
+    row[i] = r >= 0 ? p.index[tl.m0 + r] : 0;
+    if ((uint32_t)row[i] >= (uint32_t)p.a_rows) row[i] = 0;
   }
 }
 __device__ void gather_rows(const Params& p, uint32_t ring, Sync& s) {
-  const int lane = threadIdx.x & 31;
-  const int chunk = lane & 7, row0 = 32 * ((threadIdx.x >> 5) & 3) + (lane >> 3);
+  const int lane = threadIdx.x & 31, first = 32 * ((threadIdx.x >> 5) & 3);
+  const int chunk = lane & 7, row0 = first + (lane >> 3);
   int stage = 0, head = 0;  // next stage to fill, oldest stage in flight
   int flying = 0;
   uint32_t phase = 0;
   const int total = total_tiles(p);
-  auto announce = [&](int n) {  // the n oldest stages have landed
+  auto announce = [&]() {  // the oldest stage in flight, once it has landed
+    if (flying == 1) cp_async_wait<0>();
+    else if (flying == 2) cp_async_wait<1>();
+    else cp_async_wait<2>();
     fence_async_smem();
     __syncwarp();
-    for (int i = 0; i < n; ++i) {
-      if (lane == 0) mbar_arrive(smem_u32(&s.full[head]));
-      if (++head == STAGES) head = 0;
-    }
-    flying -= n;
+    if (lane == 0) mbar_arrive(smem_u32(&s.full[head]));
+    if (++head == STAGES) head = 0;
+    --flying;
   };
-  int row[8], next[8];
+  int row[8];  // of the next tile
   Tile tl{0, 0, 0, 0};
   if ((int)blockIdx.x < total) tl = decode_tile(p, blockIdx.x);
   load_index(p, tl, row0, row);
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    const uint8_t* at[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) at[i] = p.a + (int64_t)row[i] * p.n_in;
     Tile tn{0, 0, 0, 0};
     if (t + (int)gridDim.x < total) tn = decode_tile(p, t + gridDim.x);
-    load_index(p, tn, row0, next);
+    load_index(p, tn, row0, row);
     for (int kb = 0; kb < p.kb; ++kb) {
       const uint32_t empty = smem_u32(&s.empty[stage]);
-      if (flying > 0 && !__all_sync(0xffffffffu, mbar_try_wait(empty, phase ^ 1u))) {
-        cp_async_wait<0>();
-        announce(flying);
-      }
+      while (flying > 0 && (flying > IN_FLIGHT ||
+                            !__all_sync(0xffffffffu, mbar_try_wait(empty, phase ^ 1u))))
+        announce();
       if (!warp_wait(empty, phase ^ 1u, &s.abort_flag, p.status)) {
         cp_async_wait<0>();
         return;
       }
-      const uint32_t dst = ring + stage * STAGE_BYTES;
-      const int col = kb * BK + chunk * 16;
+      const uint32_t dst = ring + stage * STAGE_BYTES + row0 * BK;
+      const int col = min(kb * BK + chunk * 16, p.n_in - 16);
+      // row0 + 4 i: its last three bits alternate between two values
+      const uint32_t dst0 = dst + ((chunk ^ (row0 & 7)) << 4);
+      const uint32_t dst1 = dst + 4 * BK + ((chunk ^ ((row0 + 4) & 7)) << 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = row0 + 4 * i;
-        const bool have = col < p.n_in && (uint32_t)row[i] < (uint32_t)p.a_rows;
-        const uint8_t* src = p.a + (have ? (int64_t)row[i] * p.n_in + col : 0);
-        cp_async16(dst + r * BK + ((chunk ^ (r & 7)) << 4), src, have ? 16 : 0);
-      }
+      for (int i = 0; i < 8; ++i)
+        if (first + 4 * i < tl.rows)
+          cp_async16((i & 1 ? dst1 : dst0) + (i >> 1) * 8 * BK, at[i] + col);
       cp_async_commit();
       ++flying;
-      if (flying > IN_FLIGHT) {
-        cp_async_wait<IN_FLIGHT>();
-        announce(flying - IN_FLIGHT);
-      }
       if (++stage == STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) row[i] = next[i];
     tl = tn;
   }
-  cp_async_wait<0>();
-  announce(flying);
+  while (flying > 0) announce();
 }
 
 // Scale words of four K blocks: row r of A at byte (r % 32) * 16 + (r / 32) * 4,
@@ -322,27 +331,33 @@ __device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t sf, uint32_t
   mbar_wait(smem_u32(&s.drain), 0, &no_abort, p.status);
 }
 
-// 16-byte chunk c (0..3) of this lane's 64-byte row in the warp's staging
+// 16-byte chunk c of this lane's row (32 or 64 bytes) in the warp's staging
 // buffer, XOR-swizzled so that rows written and rows read back are free of
 // bank conflicts.
+template <int BYTES>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t st, int row, int c) {
+  return st + row * BYTES + (BYTES == 64 ? (c ^ ((row >> 1) & 3)) << 4 : (c ^ ((row >> 2) & 1)) << 4);
+}
+template <int BYTES>
 __device__ __forceinline__ void stage_chunk(uint32_t st, int c, uint4 v) {
-  const int lane = threadIdx.x & 31;
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                   st + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)),
+                   chunk_at<BYTES>(st, threadIdx.x & 31, c)),
                "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
-// Stores the staged 32 rows x 64 bytes: `rows` rows, the first `bytes` bytes.
+// Stores the staged 32 rows x BYTES: `rows` rows, the first `bytes` bytes.
+template <int BYTES>
 __device__ __forceinline__ void flush_rows(uint32_t st, char* base, int64_t ld, int rows, int bytes) {
-  const int lane = threadIdx.x & 31, c = lane & 3;
+  constexpr int CH = BYTES / 16;
+  const int lane = threadIdx.x & 31, c = lane & (CH - 1);
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = i * 8 + (lane >> 2);
+  for (int i = 0; i < CH; ++i) {
+    const int row = i * (32 / CH) + lane / CH;
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(st + row * 64 + ((c ^ ((row >> 1) & 3)) << 4))
+                 : "r"(chunk_at<BYTES>(st, row, c))
                  : "memory");
     if (row < rows && c * 16 < bytes)
       *reinterpret_cast<uint4*>(base + (int64_t)row * ld + c * 16) = v;
@@ -415,11 +430,89 @@ __device__ __forceinline__ float situ_unit(float a, float c, float b1, float b2,
   return n1 * n2 * rcp(d);
 }
 
+// A tile's hidden units of this warp: 32 rows x 32 units, quantised with the
+// maximum over the row's 128.
+__device__ __forceinline__ void finish_situ(const Params& p, const Tile& tl, float (&v)[64], int rows,
+                                            int quarter, int part, uint32_t st, uint32_t phase,
+                                            Sync& s, bool& ok) {
+  const int lane = threadIdx.x & 31;
+  float m = 0.0f;
+  if (rows > 0) {
+    float ma = 0.0f, mc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      ma = fmaxf(ma, fabsf(v[i]));
+      mc = fmaxf(mc, fabsf(v[32 + i]));
+    }
+    const float i1 = 1.0f / p.beta1, i2 = 1.0f / p.beta2;
+    if (__any_sync(0xffffffffu, ma * i1 > kGateX || mc * i2 > kUpX)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = situ_unit<true>(v[i], v[32 + i], p.beta1, p.beta2, i1, i2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = situ_unit<false>(v[i], v[32 + i], p.beta1, p.beta2, i1, i2);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));  // finite, or NaN: left out
+  }
+  s.amax[phase][quarter][part][lane] = m;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&s.quarter[quarter]));
+  ok = warp_wait(smem_u32(&s.quarter[quarter]), phase, &s.abort_flag, p.status);
+  if (!ok || rows <= 0) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, s.amax[phase][quarter][i][lane]);
+  const int e = scale_exponent(m);
+  const float inv = pow2_f(-e);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = pack_e4m3_finite(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
+                            v[4 * i + 3] * inv);
+  stage_chunk<32>(st, 0, make_uint4(w[0], w[1], w[2], w[3]));
+  stage_chunk<32>(st, 1, make_uint4(w[4], w[5], w[6], w[7]));
+  const int row0 = tl.m0 + 32 * quarter, col = tl.n * SUB + 32 * part;
+  flush_rows<32>(st, static_cast<char*>(p.out) + (int64_t)row0 * p.n_out + col, p.n_out, rows,
+                 p.n_out - col);
+  if (part == 0 && lane < rows)
+    p.out_scales[((int64_t)(tl.n >> 2) * p.rows + row0 + lane) * 4 + (tl.n & 3)] = (uint8_t)(e + 127);
+}
+
+// A plain tile's 32 rows x 128 columns of this warp.
+template <int OUT>
+__device__ __forceinline__ void finish_store(const Params& p, const Tile& tl, const float (&v)[128],
+                                             int rows, int quarter, int part, uint32_t st) {
+  constexpr int ES = OUT == OUT_F32 ? 4 : 2, CB = 64 / ES;  // columns of a 64-byte block
+  const int64_t ld = (int64_t)p.n_out * ES;
+  char* base = static_cast<char*>(p.out) + (int64_t)(tl.m0 + 32 * quarter) * ld;
+#pragma unroll
+  for (int b = 0; b < SUB / CB; ++b) {
+    const int col = tl.n * 2 * SUB + SUB * part + b * CB;
+    if (rows > 0 && col < p.n_out) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float* f = v + b * CB + c * (16 / ES);
+        stage_chunk<64>(st, c,
+                        OUT == OUT_F32
+                            ? make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
+                                         __float_as_uint(f[2]), __float_as_uint(f[3]))
+                            : make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
+                                         bf16x2(f[6], f[7])));
+      }
+      flush_rows<64>(st, base + (int64_t)col * ES, ld, rows, (p.n_out - col) * ES);
+    }
+  }
+}
+
 template <int OUT>
 __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sync& s) {
+  using C = Cfg<OUT>;
   const int lane = threadIdx.x & 31, ew = (threadIdx.x >> 5) - EPI_WARP0;
-  const int quarter = (threadIdx.x >> 5) & 3, half = ew >> 2;  // TMEM lanes 32 (warp mod 4) ...
-  const uint32_t st = stage_base + ew * EPI_STAGE;
+  const int quarter = ew & 3, part = ew >> 2;  // TMEM lanes 32 (warp mod 4) ..., columns
+  const uint32_t st = stage_base + ew * C::EPI_STAGE;
+  const uint32_t ta = tmem + ((uint32_t)(32 * quarter) << 16);
   uint32_t phase = 0;
   const int total = total_tiles(p);
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
@@ -427,17 +520,14 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
     const int rows = min(32, tl.rows - 32 * quarter);
     if (!warp_wait(smem_u32(&s.tfull), phase, &s.abort_flag, p.status)) return;
     fence_after();
-    float v[128];
-    const uint32_t ta = tmem + ((uint32_t)(32 * quarter) << 16);
+    float v[OUT == OUT_SITU ? 64 : 128];
     if (rows > 0) {
       if (OUT == OUT_SITU) {
-        ld32(ta + 64 * half, v);
-        ld32(ta + 64 * half + 32, v + 32);
-        ld32(ta + SUB + 64 * half, v + 64);
-        ld32(ta + SUB + 64 * half + 32, v + 96);
+        ld32(ta + 32 * part, v);
+        ld32(ta + SUB + 32 * part, v + 32);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ld32(ta + SUB * half + 32 * i, v + 32 * i);
+        for (int i = 0; i < 4; ++i) ld32(ta + SUB * part + 32 * i, v + 32 * i);
       }
       ld_wait();
     }
@@ -445,94 +535,28 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
     fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.tempty));
-    const int row0 = tl.m0 + 32 * quarter;
-    if (OUT == OUT_SITU) {
-      float m = 0.0f;
-      if (rows > 0) {
-        float ma = 0.0f, mc = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          ma = fmaxf(ma, fabsf(v[i]));
-          mc = fmaxf(mc, fabsf(v[64 + i]));
-        }
-        const float i1 = 1.0f / p.beta1, i2 = 1.0f / p.beta2;
-        if (__any_sync(0xffffffffu, ma * i1 > kGateX || mc * i2 > kUpX)) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            v[i] = situ_unit<true>(v[i], v[64 + i], p.beta1, p.beta2, i1, i2);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            v[i] = situ_unit<false>(v[i], v[64 + i], p.beta1, p.beta2, i1, i2);
-        }
-#pragma unroll
-        for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(v[i]));  // finite, or NaN: left out
-      }
-      s.amax[phase][ew][lane] = m;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.pair[quarter]));
-      if (!warp_wait(smem_u32(&s.pair[quarter]), phase, &s.abort_flag, p.status)) return;
-      if (rows > 0) {
-        m = fmaxf(m, s.amax[phase][ew ^ 4][lane]);
-        const int e = scale_exponent(m);
-        const float inv = pow2_f(-e);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float* f = v + 16 * c;
-          uint4 w;
-          w.x = pack_e4m3_finite(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-          w.y = pack_e4m3_finite(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-          w.z = pack_e4m3_finite(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv);
-          w.w = pack_e4m3_finite(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv);
-          stage_chunk(st, c, w);
-        }
-        const int col = tl.n * SUB + 64 * half;
-        flush_rows(st, static_cast<char*>(p.out) + (int64_t)row0 * p.n_out + col, p.n_out, rows,
-                   min(64, p.n_out - col));
-        if (half == 0 && lane < rows)
-          p.out_scales[((int64_t)(tl.n >> 2) * p.rows + row0 + lane) * 4 + (tl.n & 3)] =
-              (uint8_t)(e + 127);
-      }
-    } else if (rows > 0) {
-      constexpr int ES = OUT == OUT_F32 ? 4 : 2, CB = 64 / ES;  // columns of a 64-byte block
-      const int col0 = tl.n * 2 * SUB + SUB * half;
-      const int64_t ld = (int64_t)p.n_out * ES;
-      char* base = static_cast<char*>(p.out) + (int64_t)row0 * ld;
-#pragma unroll
-      for (int b = 0; b < SUB / CB; ++b) {
-        const int col = col0 + b * CB;
-        if (col < p.n_out) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float* f = v + b * CB + c * (16 / ES);
-            uint4 w;
-            if (OUT == OUT_F32)
-              w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                             __float_as_uint(f[3]));
-            else
-              w = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
-                             bf16x2(f[6], f[7]));
-            stage_chunk(st, c, w);
-          }
-          flush_rows(st, base + (int64_t)col * ES, ld, rows, min(CB, p.n_out - col) * ES);
-        }
-      }
+    if constexpr (OUT == OUT_SITU) {
+      bool ok;
+      finish_situ(p, tl, v, rows, quarter, part, st, phase, s, ok);
+      if (!ok) return;
+    } else {
+      finish_store<OUT>(p, tl, v, rows, quarter, part, st);
     }
     phase ^= 1u;
   }
 }
 
 template <int OUT>
-__global__ void __launch_bounds__(kThreads<OUT>, 1) experts_fp8_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<OUT>::THREADS, 1) experts_fp8_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync s;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t stage_base = ring + STAGES * STAGE_BYTES;
-  const uint32_t sf = stage_base + EPI_WARPS * EPI_STAGE;
+  const uint32_t sf = stage_base + EPI_BYTES;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&s.full[i]), OUT == OUT_SITU ? 1 + GATHER_WARPS : 1);
+      mbar_init(smem_u32(&s.full[i]), 1 + Cfg<OUT>::GATHER_WARPS);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < SF_STAGES; ++i) {
@@ -540,9 +564,9 @@ __global__ void __launch_bounds__(kThreads<OUT>, 1) experts_fp8_kernel(const __g
       mbar_init(smem_u32(&s.sempty[i]), 1);
     }
     mbar_init(smem_u32(&s.tfull), 1);
-    mbar_init(smem_u32(&s.tempty), EPI_WARPS);
+    mbar_init(smem_u32(&s.tempty), Cfg<OUT>::EPI_WARPS);
     mbar_init(smem_u32(&s.drain), 1);
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.pair[i]), 2);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.quarter[i]), Cfg<OUT>::SPLIT);
     s.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -570,7 +594,7 @@ __global__ void __launch_bounds__(kThreads<OUT>, 1) experts_fp8_kernel(const __g
     } else if (warp == 2) {
       produce_scales<OUT>(p, sf, s);
     }
-  } else if (warp < EPI_WARP0 + EPI_WARPS) {
+  } else if (warp < Cfg<OUT>::GATHER_WARP0) {
     if (OUT == OUT_SITU) regs_inc<REGS_EPI>();
     epilogue<OUT>(p, tmem, stage_base, s);
   } else if (OUT == OUT_SITU) {
@@ -653,7 +677,7 @@ cudaError_t launch(const Params& p, int64_t max_tiles, cudaStream_t st) {
   const int grid = (int)std::min<int64_t>(max_tiles * p.n_tiles, sms);
   if (grid <= 0) return cudaSuccess;
   count_launch();
-  return launch_pdl(experts_fp8_kernel<OUT>, dim3(grid), dim3(kThreads<OUT>), (size_t)SMEM_BYTES, st, 1,
+  return launch_pdl(experts_fp8_kernel<OUT>, dim3(grid), dim3(Cfg<OUT>::THREADS), (size_t)SMEM_BYTES, st, 1,
                     p);
 }
 
