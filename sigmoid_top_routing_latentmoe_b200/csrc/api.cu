@@ -318,8 +318,17 @@ static lmoe_status run_route_grouped(const lmoe_dims* d, const RouteRule& rule, 
 }
 
 // ------------------------------------------------------- 8-bit routed experts
+static bool fp8_pairs(const lmoe_dims* d) {
+  if (const char* v = getenv("LMOE_FP8_PAIRS")) {
+    if (v[0] == '0') return false;
+    if (v[0] == '1') return true;
+  }
+  return d->n_tokens * (int64_t)d->top_k >= 256 * (int64_t)d->n_routed;
+}
+
 static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* offsets, void* ws) {
   TileList t;
+  t.tile_m = fp8_pairs(d) ? kRoutedPairTileM : kTileM;
   t.offsets = offsets; t.R = d->n_routed; t.rows = d->n_tokens * d->top_k;
   t.max_tiles = L.max_tiles;
   t.n_mtiles = &at<WsHeader>(ws, L.header)->n_mtiles;
@@ -355,6 +364,7 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   }
   Fp8Gemm g{};
   g.rows = P; g.R = d->n_routed; g.tiles = tl.tiles; g.n_mtiles = tl.n_mtiles;
+  g.pairs = tl.tile_m == kRoutedPairTileM;
   g.max_tiles = tl.max_tiles; g.beta1 = d->beta1; g.beta2 = d->beta2;
   {
     ProfScope ps("expert_gemm1", st);
@@ -1094,6 +1104,7 @@ lmoe_status moe_expert_gemm_fp8(const lmoe_dims* dims, int32_t n_in, int32_t n_o
   g.a = (const uint8_t*)a; g.a_scales = a_scales; g.a_rows = g.rows = tl.rows; g.R = dims->n_routed;
   g.n_in = n_in; g.n_out = n_out; g.w = (const uint8_t*)w; g.w_scales = w_scales; g.out = out;
   g.out_f32 = dims->dtype == LMOE_F32 ? 1 : 0;
+  g.pairs = tl.tile_m == kRoutedPairTileM;
   if (offsets != nullptr) {
     g.tiles = tl.tiles; g.n_mtiles = tl.n_mtiles; g.max_tiles = tl.max_tiles;
     LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");

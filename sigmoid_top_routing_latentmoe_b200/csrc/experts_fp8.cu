@@ -5,8 +5,8 @@
 // for 32 elements of K: a block's byte serves its four K steps), so the sum
 // over all of K stays in one fp32 TMEM accumulator.
 //
-// One persistent, warp-specialised kernel; a tile is 128 rows of one expert x
-// 256 columns (SiTU: 128 gate and the 128 matching up columns), K in blocks of
+// One persistent, warp-specialised kernel; a tile is 128 rows of one expert (256
+// on a CTA pair) x 256 columns (SiTU: 128 gate and the 128 matching up columns), K in blocks of
 // 128 (one 128-byte swizzle row):
 //   warp 0     TMA producer: A rows and two 128-row B boxes per K block,
 //   warp 1     MMA issuer and TMEM allocator; every fourth K block it also
@@ -33,35 +33,41 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 128, SUB = 128, BK = 128;
-constexpr int A_BYTES = BM * BK, B_BYTES = 2 * SUB * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int STAGES = 4;
+constexpr int A_BYTES = BM * BK, SUB_BYTES = SUB * BK;
 constexpr int SMALL_ROWS = 32;            // tiles of at most this many rows load a smaller A box
 constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
 constexpr int SF_BYTES = 3 * 512;         // A words, then two blocks of B words
 constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
+constexpr int TMEM_COLS = 512, SF_COL0 = 256;
 constexpr int EPI_WARP0 = 4;
+constexpr int EPI_BYTES = 8 * 32 * 64;    // staging of all epilogue warps
+static_assert(SF_COL0 + SF_STAGES * SF_COLS <= TMEM_COLS, "TMEM");
 enum Out { OUT_BF16 = 0, OUT_F32 = 1, OUT_SITU = 2 };
-// Epilogue warps share a 32-row quarter of the tile by columns.  Plain tiles: 2
-// warps with 128 columns each; SiTU tiles: 4 warps with 32 hidden units each,
-// whose 64 accumulators leave the compiler room to overlap the units (with 2
-// warps and 128 accumulators the mid layer's product took 426 us).
-template <int OUT>
+
+// CG = 1: a CTA computes a 128-row tile and loads both B boxes of a K block.
+// CG = 2: a CTA pair (cluster of 2) computes a 256-row tile; each CTA loads its
+//   own 128 rows of A, one of the two B boxes and its own scale words, and the
+//   leader (rank 0) issues the MMAs of both.
+// Epilogue warps share a 32-row quarter of a CTA's rows by columns.  Plain tiles:
+// 2 warps with 128 columns each; SiTU tiles: 4 warps with 32 hidden units each,
+// whose 64 accumulators leave the compiler room to overlap the units.
+template <int OUT, int CG>
 struct Cfg {
-  static constexpr int SPLIT = OUT == OUT_SITU ? 4 : 2;   // warps per quarter
+  static constexpr int STAGE_BYTES = A_BYTES + (CG == 1 ? 2 : 1) * SUB_BYTES;
+  static constexpr int STAGES = CG == 1 ? 4 : 6;
+  static constexpr int SPLIT = OUT == OUT_SITU ? 4 : 2;   // epilogue warps per quarter
   static constexpr int EPI_WARPS = 4 * SPLIT;
+  static constexpr int EPI_STAGE = 32 * (OUT == OUT_SITU ? 32 : 64);  // bytes per warp
   static constexpr int GATHER_WARP0 = EPI_WARP0 + EPI_WARPS;
   static constexpr int GATHER_WARPS = OUT == OUT_SITU ? 4 : 0;
   static constexpr int THREADS = 32 * (GATHER_WARP0 + GATHER_WARPS);
-  static constexpr int EPI_STAGE = 32 * (OUT == OUT_SITU ? 32 : 64);  // bytes per warp
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + SF_STAGES * SF_BYTES + 1024;
 };
-constexpr int EPI_BYTES = 8 * 32 * 64;    // staging of all epilogue warps
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + SF_STAGES * SF_BYTES + 1024;
+static_assert(Cfg<OUT_SITU, 1>::SMEM_BYTES + 5 * 1024 <= 232448, "shared memory");
+static_assert(Cfg<OUT_SITU, 2>::SMEM_BYTES + 5 * 1024 <= 232448, "shared memory");
 // The SiTU kernel's 768 threads start with 80 registers each; its 16 epilogue
 // warps take what the other 8 give up (512 x 96 + 256 x 48 = 768 x 80).
 constexpr int REGS_EPI = 96, REGS_OTHER = 48;
-constexpr int TMEM_COLS = 512, SF_COL0 = 256;
-static_assert(SMEM_BYTES <= 232448, "shared memory");
-static_assert(SF_COL0 + SF_STAGES * SF_COLS <= TMEM_COLS, "TMEM");
 
 struct Params {
   CUtensorMap tmA, tmA32, tmB0, tmB1;
@@ -79,27 +85,46 @@ struct Params {
   float beta1, beta2;
 };
 
+// This CTA (or its pair): which of the tiles it takes, and its rank in the pair.
+struct Unit {
+  int first, step, rank;
+};
+// A tile, or a CTA's share of its rows: [m0, m0 + rows) of expert e, column tile n.
 struct Tile {
   int e, m0, rows, n;
 };
+template <int CG>
 __device__ __forceinline__ int total_tiles(const Params& p) {
-  return (p.tiles != nullptr ? *p.n_mtiles : (p.rows + BM - 1) / BM) * p.n_tiles;
+  return (p.tiles != nullptr ? *p.n_mtiles : (p.rows + BM * CG - 1) / (BM * CG)) * p.n_tiles;
 }
+template <int CG>
 __device__ __forceinline__ Tile decode_tile(const Params& p, int t) {
   const int mt = t / p.n_tiles, n = t - mt * p.n_tiles;
-  if (p.tiles == nullptr) return {0, mt * BM, min(BM, p.rows - mt * BM), n};
+  if (p.tiles == nullptr) return {0, mt * BM * CG, min(BM * CG, p.rows - mt * BM * CG), n};
   const int4 e = p.tiles[mt];
   return {e.x, e.y, e.z, n};
 }
-// Whether a plain tile has a second 128-column half.
-template <int OUT>
+// Tile t, which a role asks for one tile ahead so that its load is over when
+// the tile's turn comes (each role waiting for it in turn cost some 1000 cycles
+// a tile); any tile behind the last.
+template <int CG>
+__device__ __forceinline__ Tile tile_ahead(const Params& p, int t, int total) {
+  return t < total ? decode_tile<CG>(p, t) : Tile{0, 0, 0, 0};
+}
+template <int CG>
+__device__ __forceinline__ Tile own_rows(const Tile& t, int rank) {
+  if (CG == 1) return t;
+  return {t.e, t.m0 + BM * rank, min(BM, max(0, t.rows - BM * rank)), t.n};
+}
+// Whether a plain tile of a single CTA has a second 128-column half (a pair's
+// second box may lie outside W: it loads zeros).
+template <int OUT, int CG>
 __device__ __forceinline__ bool two_subs(const Params& p, const Tile& tl) {
-  return OUT == OUT_SITU || tl.n * 2 * SUB + SUB < p.n_out;
+  return OUT == OUT_SITU || CG == 2 || tl.n * 2 * SUB + SUB < p.n_out;
 }
 
 struct Sync {
-  uint64_t full[STAGES], empty[STAGES], sfull[SF_STAGES], sempty[SF_STAGES], tfull, tempty, drain,
-      quarter[4];
+  uint64_t full[6], empty[6], sfull[SF_STAGES], sempty[SF_STAGES], tfull, tempty, drain, quarter[4];
   float amax[2][4][4][32];  // tile parity, quarter, warp of the quarter, row
   uint32_t tmem;
   volatile int abort_flag;
@@ -107,47 +132,58 @@ struct Sync {
 
 // The SiTU product takes its rows of A through p.index (gather_rows), the
 // others their neighbouring rows by TMA.
-template <int OUT>
-__device__ void produce(const Params& p, uint32_t ring, Sync& s) {
+template <int OUT, int CG>
+__device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
+  using C = Cfg<OUT, CG>;
   constexpr bool GATHER = OUT == OUT_SITU;
   int stage = 0;
   uint32_t phase = 0, issued = 0, issued_phase = 0;
   bool ok = true;
-  const int total = total_tiles(p);
-  for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-    const Tile tl = decode_tile(p, t);
-    const bool small = tl.rows <= SMALL_ROWS, two = two_subs<OUT>(p, tl);
+  const int total = total_tiles<CG>(p);
+  const uint32_t full0 = smem_u32(s.full), lead0 = CG == 1 ? full0 : map_to_rank(full0, 0);
+  Tile next = tile_ahead<CG>(p, u.first, total);
+  for (int t = u.first; ok && t < total; t += u.step) {
+    const Tile tl = next;
+    next = tile_ahead<CG>(p, t + u.step, total);
+    const bool small = CG == 1 && tl.rows <= SMALL_ROWS, two = two_subs<OUT, CG>(p, tl);
     const CUtensorMap* map_a = small ? &p.tmA32 : &p.tmA;
-    const CUtensorMap* map_b1 = OUT == OUT_SITU ? &p.tmB1 : &p.tmB0;
+    // a pair's second CTA loads no A when it has no rows (its accumulator is not stored)
+    const bool load_a = !GATHER && (u.rank == 0 || tl.rows > BM);
+    const int a_ctas = GATHER ? 0 : CG == 2 && tl.rows > BM ? 2 : 1;
+    const uint32_t bytes = a_ctas * (small ? SMALL_ROWS * BK : A_BYTES) + (two ? 2 : 1) * SUB_BYTES;
+    // this CTA's boxes of W: gate and up, or two neighbouring boxes; of a pair, each CTA one
     const int row0 = OUT == OUT_SITU ? tl.n * SUB : tl.n * 2 * SUB;
     const int row1 = OUT == OUT_SITU ? row0 : row0 + SUB;
-    const uint32_t bytes =
-        (GATHER ? 0 : small ? SMALL_ROWS * BK : A_BYTES) + (two ? B_BYTES : B_BYTES / 2);
+    const CUtensorMap* map1 = OUT == OUT_SITU ? &p.tmB1 : &p.tmB0;
+    const CUtensorMap* map_b = u.rank == 0 ? &p.tmB0 : map1;
+    const int row_b = u.rank == 0 ? row0 : row1;
     for (int kb = 0; kb < p.kb; ++kb) {
       if (!mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, &s.abort_flag, p.status)) {
         ok = false;
         break;
       }
-      const uint32_t dst = ring + stage * STAGE_BYTES, bar = smem_u32(&s.full[stage]);
-      mbar_expect_tx(bar, bytes);
-      if (!GATHER) tma_load_2d(dst, map_a, bar, kb * BK, tl.m0);
-      tma_load_3d(dst + A_BYTES, &p.tmB0, bar, kb * BK, row0, tl.e);
-      if (two) tma_load_3d(dst + A_BYTES + SUB * BK, map_b1, bar, kb * BK, row1, tl.e);
+      const uint32_t dst = ring + stage * C::STAGE_BYTES, bar = lead0 + 8 * stage;
+      if (u.rank == 0) mbar_expect_tx(full0 + 8 * stage, bytes);
+      if (load_a) tma_load_2d<CG>(dst, map_a, bar, kb * BK, tl.m0 + BM * u.rank);
+      tma_load_3d<CG>(dst + A_BYTES, map_b, bar, kb * BK, row_b, tl.e);
+      if (CG == 1 && two) tma_load_3d<CG>(dst + A_BYTES + SUB_BYTES, map1, bar, kb * BK, row1, tl.e);
       issued |= 1u << stage;
       issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-      if (++stage == STAGES) {
+      if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
   }
-  // every load issued has landed before the block exits (a stage's barrier may
-  // still lack the gather warp's arrival after an abort: then the cap ends the wait)
-  for (int i = 0; i < STAGES; ++i)
-    if (issued & (1u << i)) {
-      volatile int no_abort = 0;
-      mbar_wait(smem_u32(&s.full[i]), (issued_phase >> i) & 1u, &no_abort, p.status);
-    }
+  // every load issued has landed before the block exits (a pair's loads land on
+  // the leader's barriers).  After an abort a stage may lack other arrivals:
+  // then the cap ends the wait.
+  if (u.rank == 0)
+    for (int i = 0; i < C::STAGES; ++i)
+      if (issued & (1u << i)) {
+        volatile int no_abort = 0;
+        mbar_wait(full0 + 8 * i, (issued_phase >> i) & 1u, &no_abort, p.status);
+      }
 }
 
 // Rows of A by index, four warps with 32 rows each, by 16-byte asynchronous
@@ -155,10 +191,10 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s) {
 // announced once its copies have landed; up to IN_FLIGHT stages stay in
 // flight, but none while the ring is full, when the tensor cores may be
 // waiting for exactly these.  Every copy reads inside its row, so that none
-// needs zero-filling (whose branches took four times as long): columns past
-// n_in repeat the last ones (they meet zeros of W), rows past the tile repeat
-// its last row (never stored), and an index outside A reads row 0 (its scale
-// words are 0, and so is its product).
+// needs zero-filling (whose branches took longer): columns past n_in repeat
+// the last ones (they meet zeros of W), rows past the tile repeat its last row
+// (never stored), and an index outside A reads row 0 (its scale words are 0,
+// and so is its product).
 constexpr int IN_FLIGHT = 2;
 __device__ __forceinline__ void load_index(const Params& p, const Tile& tl, int row0, int (&row)[8]) {
 #pragma unroll
@@ -168,34 +204,39 @@ __device__ __forceinline__ void load_index(const Params& p, const Tile& tl, int 
     if ((uint32_t)row[i] >= (uint32_t)p.a_rows) row[i] = 0;
   }
 }
-__device__ void gather_rows(const Params& p, uint32_t ring, Sync& s) {
+template <int CG>
+__device__ void gather_rows(const Params& p, uint32_t ring, Sync& s, Unit u) {
+  using C = Cfg<OUT_SITU, CG>;
   const int lane = threadIdx.x & 31, first = 32 * ((threadIdx.x >> 5) & 3);
   const int chunk = lane & 7, row0 = first + (lane >> 3);
   int stage = 0, head = 0;  // next stage to fill, oldest stage in flight
   int flying = 0;
   uint32_t phase = 0;
-  const int total = total_tiles(p);
+  const int total = total_tiles<CG>(p);
+  const uint32_t lead0 = CG == 1 ? smem_u32(s.full) : map_to_rank(smem_u32(s.full), 0);
   auto announce = [&]() {  // the oldest stage in flight, once it has landed
     if (flying == 1) cp_async_wait<0>();
     else if (flying == 2) cp_async_wait<1>();
     else cp_async_wait<2>();
-    fence_async_smem();
+    fence_async_smem<CG>();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.full[head]));
-    if (++head == STAGES) head = 0;
+    if (lane == 0) {
+      if (CG == 1) mbar_arrive(lead0 + 8 * head);
+      else mbar_arrive_cluster(lead0 + 8 * head);
+    }
+    if (++head == C::STAGES) head = 0;
     --flying;
   };
   int row[8];  // of the next tile
-  Tile tl{0, 0, 0, 0};
-  if ((int)blockIdx.x < total) tl = decode_tile(p, blockIdx.x);
+  Tile tl = own_rows<CG>(tile_ahead<CG>(p, u.first, total), u.rank);
+  Tile tn = own_rows<CG>(tile_ahead<CG>(p, u.first + u.step, total), u.rank);
   load_index(p, tl, row0, row);
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+  for (int t = u.first; t < total; t += u.step) {
     const uint8_t* at[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) at[i] = p.a + (int64_t)row[i] * p.n_in;
-    Tile tn{0, 0, 0, 0};
-    if (t + (int)gridDim.x < total) tn = decode_tile(p, t + gridDim.x);
     load_index(p, tn, row0, row);
+    const Tile after = own_rows<CG>(tile_ahead<CG>(p, t + 2 * u.step, total), u.rank);
     for (int kb = 0; kb < p.kb; ++kb) {
       const uint32_t empty = smem_u32(&s.empty[stage]);
       while (flying > 0 && (flying > IN_FLIGHT ||
@@ -205,7 +246,7 @@ __device__ void gather_rows(const Params& p, uint32_t ring, Sync& s) {
         cp_async_wait<0>();
         return;
       }
-      const uint32_t dst = ring + stage * STAGE_BYTES + row0 * BK;
+      const uint32_t dst = ring + stage * C::STAGE_BYTES + row0 * BK;
       const int col = min(kb * BK + chunk * 16, p.n_in - 16);
       // row0 + 4 i: its last three bits alternate between two values
       const uint32_t dst0 = dst + ((chunk ^ (row0 & 7)) << 4);
@@ -216,117 +257,158 @@ __device__ void gather_rows(const Params& p, uint32_t ring, Sync& s) {
           cp_async16((i & 1 ? dst1 : dst0) + (i >> 1) * 8 * BK, at[i] + col);
       cp_async_commit();
       ++flying;
-      if (++stage == STAGES) {
+      if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
     tl = tn;
+    tn = after;
   }
   while (flying > 0) announce();
 }
 
 // Scale words of four K blocks: row r of A at byte (r % 32) * 16 + (r / 32) * 4,
 // so that tcgen05.cp puts it in lane r % 32, column r / 32; a weight block has
-// one word for its 128 rows.
-template <int OUT>
-__device__ void produce_scales(const Params& p, uint32_t sf, Sync& s) {
+// one word for its 128 rows.  Each CTA of a pair prepares its own rows' words
+// and those of both weight blocks.  The words are loaded one step ahead, a
+// tile's row numbers one tile ahead: loaded when needed, they held the tensor
+// cores up (450 instead of 400 ns a K block on single CTAs, 437 / 374 on pairs).
+struct ScaleRows {
+  int row[4];                // rows of A, -1: none (its product is not stored, or of zeros)
+  const uint32_t *w0, *w1;   // words of the two weight blocks
+};
+struct ScaleWords {
+  uint32_t a[4], b0, b1;
+};
+template <int OUT, int CG>
+__device__ __forceinline__ ScaleRows scale_rows(const Params& p, int t, int total, const Unit& u) {
+  const int lane = threadIdx.x & 31;
+  ScaleRows r{{-1, -1, -1, -1}, nullptr, nullptr};
+  if (t >= total) return r;
+  const Tile tl = own_rows<CG>(decode_tile<CG>(p, t), u.rank);
+  const int nb0 = OUT == OUT_SITU ? tl.n : 2 * tl.n;
+  const int64_t at = ((int64_t)tl.e * p.w_blocks + nb0) * p.words;
+  r.w0 = p.w_words + at;
+  r.w1 = OUT == OUT_SITU ? p.w_up_words + at : nb0 + 1 < p.w_blocks ? r.w0 + p.words : r.w0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = lane + 32 * j;
+    if (i < tl.rows) r.row[j] = OUT == OUT_SITU ? p.index[tl.m0 + i] : tl.m0 + i;
+    if (r.row[j] >= p.a_rows) r.row[j] = -1;
+  }
+  return r;
+}
+__device__ __forceinline__ ScaleWords scale_words(const Params& p, const ScaleRows& r, int q) {
+  ScaleWords w{{0, 0, 0, 0}, 0, 0};
+  if (r.w0 == nullptr) return w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (r.row[j] >= 0) w.a[j] = p.a_words[(int64_t)q * p.a_rows + r.row[j]];
+  w.b0 = r.w0[q];
+  w.b1 = r.w1[q];
+  return w;
+}
+template <int OUT, int CG>
+__device__ void produce_scales(const Params& p, uint32_t sf, Sync& s, Unit u) {
   const int lane = threadIdx.x & 31;
   int stage = 0;
   uint32_t phase = 0;
-  const int total = total_tiles(p);
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const Tile tl = decode_tile(p, t);
-    const bool two = two_subs<OUT>(p, tl);
-    const int nb0 = OUT == OUT_SITU ? tl.n : 2 * tl.n;
-    const uint32_t* w0 = p.w_words + ((int64_t)tl.e * p.w_blocks + nb0) * p.words;
-    const uint32_t* w1 =
-        OUT == OUT_SITU ? p.w_up_words + ((int64_t)tl.e * p.w_blocks + nb0) * p.words : w0 + p.words;
-    int row[4];  // rows of A, -1: none (its product is not stored, or of zeros)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = lane + 32 * j;
-      row[j] = r >= tl.rows ? -1 : OUT == OUT_SITU ? p.index[tl.m0 + r] : tl.m0 + r;
-      if (row[j] >= p.a_rows) row[j] = -1;
-    }
+  const int total = total_tiles<CG>(p);
+  const uint32_t lead0 = CG == 1 ? smem_u32(s.sfull) : map_to_rank(smem_u32(s.sfull), 0);
+  ScaleRows rows = scale_rows<OUT, CG>(p, u.first, total, u);
+  ScaleWords next = scale_words(p, rows, 0);
+  for (int t = u.first; t < total; t += u.step) {
+    const ScaleRows rows1 = scale_rows<OUT, CG>(p, t + u.step, total, u);
     for (int q = 0; q < p.words; ++q) {
-      uint32_t a[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        a[j] = row[j] >= 0 ? p.a_words[(int64_t)q * p.a_rows + row[j]] : 0u;
-      const uint32_t b0 = w0[q], b1 = two ? w1[q] : 0u;
+      const ScaleWords w = next;
+      next = q + 1 < p.words ? scale_words(p, rows, q + 1) : scale_words(p, rows1, 0);
       if (!warp_wait(smem_u32(&s.sempty[stage]), phase ^ 1u, &s.abort_flag, p.status)) return;
       const uint32_t dst = sf + stage * SF_BYTES + lane * 16;
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a[0]), "r"(a[1]),
-                   "r"(a[2]), "r"(a[3])
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.a[0]), "r"(w.a[1]),
+                   "r"(w.a[2]), "r"(w.a[3])
                    : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + 512), "r"(b0) : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + 1024), "r"(b1) : "memory");
-      fence_async_smem();
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + 512), "r"(w.b0) : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + 1024), "r"(w.b1) : "memory");
+      fence_async_smem<CG>();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.sfull[stage]));
+      if (lane == 0) {
+        if (CG == 1) mbar_arrive(lead0 + 8 * stage);
+        else mbar_arrive_cluster(lead0 + 8 * stage);
+      }
       if (++stage == SF_STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
+    rows = rows1;
   }
 }
 
-template <int OUT>
-__device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t sf, uint32_t tmem, Sync& s) {
+// The whole warp walks the tiles, so that addresses and descriptors stay in
+// uniform registers, and one elected lane issues (a single lane walking alone
+// took about 700 cycles a K block to issue what the tensor cores do in 512).
+template <int OUT, int CG>
+__device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t sf, uint32_t tmem, Sync& s,
+                           Unit u) {
+  using C = Cfg<OUT, CG>;
+  constexpr bool PAIR = CG == 2;
   int stage = 0, sstage = 0;
   uint32_t phase = 0, sphase = 0, tphase = 0;
   bool ok = true;
-  const int total = total_tiles(p);
-  for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-    const Tile tl = decode_tile(p, t);
-    const bool two = two_subs<OUT>(p, tl);
-    const uint32_t idesc = instr_desc_mxf8(two ? 2 * SUB : SUB);
-    if (!mbar_wait(smem_u32(&s.tempty), tphase ^ 1u, &s.abort_flag, p.status)) break;
+  const int total = total_tiles<CG>(p);
+  Tile next = tile_ahead<CG>(p, u.first, total);
+  for (int t = u.first; ok && t < total; t += u.step) {
+    const bool two = two_subs<OUT, CG>(p, next);
+    next = tile_ahead<CG>(p, t + u.step, total);
+    const uint32_t idesc = instr_desc_mxf8<CG>(two ? 2 * SUB : SUB);
+    if (!warp_wait<PAIR>(smem_u32(&s.tempty), tphase ^ 1u, &s.abort_flag, p.status)) break;
     tphase ^= 1u;
     fence_after();
     for (int kb = 0; kb < p.kb; ++kb) {
       const uint32_t sfa = tmem + SF_COL0 + sstage * SF_COLS, sfb = sfa + 4;
       if ((kb & 3) == 0) {
-        if (!mbar_wait(smem_u32(&s.sfull[sstage]), sphase, &s.abort_flag, p.status)) {
+        if (!warp_wait<PAIR>(smem_u32(&s.sfull[sstage]), sphase, &s.abort_flag, p.status)) {
           ok = false;
           break;
         }
         fence_after();
-        const uint32_t src = sf + sstage * SF_BYTES;
-        cp_scales(sfa, desc_scales(src));
-        cp_scales(sfb, desc_scales(src + 512));
-        if (two) cp_scales(sfb + 4, desc_scales(src + 1024));
+        const uint64_t src = desc_scales(sf + sstage * SF_BYTES);
+        if (elect_one()) {
+          cp_scales<CG>(sfa, src);
+          cp_scales<CG>(sfb, src + (512 >> 4));
+          if (two) cp_scales<CG>(sfb + 4, src + (1024 >> 4));
+        }
       }
-      if (!mbar_wait(smem_u32(&s.full[stage]), phase, &s.abort_flag, p.status)) {
+      if (!warp_wait<PAIR>(smem_u32(&s.full[stage]), phase, &s.abort_flag, p.status)) {
         ok = false;
         break;
       }
       fence_after();
-      const uint32_t a = ring + stage * STAGE_BYTES, b = a + A_BYTES;
+      const uint64_t a = desc_sw128(ring + stage * C::STAGE_BYTES), b = a + (A_BYTES >> 4);
       const uint32_t id = idesc | sf_id_bits(kb & 3);
+      const bool last = kb == p.kb - 1;
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < BK / 32; ++k)
-        mma_mxf8(tmem, desc_sw128(a + k * 32), desc_sw128(b + k * 32), id, sfa, sfb,
-                 (kb > 0 || k > 0) ? 1u : 0u);
-      commit(smem_u32(&s.empty[stage]));
-      if (++stage == STAGES) {
+        for (int k = 0; k < BK / 32; ++k)
+          mma_mxf8<CG>(tmem, a + 2 * k, b + 2 * k, id, sfa, sfb, (kb > 0 || k > 0) ? 1u : 0u);
+        commit<CG>(smem_u32(&s.empty[stage]));
+        if ((kb & 3) == 3 || last) commit<CG>(smem_u32(&s.sempty[sstage]));
+        if (last) commit<CG>(smem_u32(&s.tfull));
+      }
+      if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
-      if ((kb & 3) == 3 || kb == p.kb - 1) {
-        commit(smem_u32(&s.sempty[sstage]));
+      if ((kb & 3) == 3 || last) {
         if (++sstage == SF_STAGES) {
           sstage = 0;
           sphase ^= 1u;
         }
       }
     }
-    if (!ok) break;
-    commit(smem_u32(&s.tfull));
   }
-  commit(smem_u32(&s.drain));  // all MMAs are complete before TMEM is freed
+  if (elect_one()) commit<CG>(smem_u32(&s.drain));  // all MMAs are complete before TMEM is freed
   volatile int no_abort = 0;
   mbar_wait(smem_u32(&s.drain), 0, &no_abort, p.status);
 }
@@ -506,17 +588,21 @@ __device__ __forceinline__ void finish_store(const Params& p, const Tile& tl, co
   }
 }
 
-template <int OUT>
-__device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sync& s) {
-  using C = Cfg<OUT>;
+template <int OUT, int CG>
+__device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sync& s, Unit u) {
+  using C = Cfg<OUT, CG>;
   const int lane = threadIdx.x & 31, ew = (threadIdx.x >> 5) - EPI_WARP0;
   const int quarter = ew & 3, part = ew >> 2;  // TMEM lanes 32 (warp mod 4) ..., columns
   const uint32_t st = stage_base + ew * C::EPI_STAGE;
   const uint32_t ta = tmem + ((uint32_t)(32 * quarter) << 16);
+  // the leader's MMA thread waits for the epilogues of both CTAs
+  const uint32_t tempty = CG == 1 ? smem_u32(&s.tempty) : map_to_rank(smem_u32(&s.tempty), 0);
   uint32_t phase = 0;
-  const int total = total_tiles(p);
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const Tile tl = decode_tile(p, t);
+  const int total = total_tiles<CG>(p);
+  Tile next = tile_ahead<CG>(p, u.first, total);
+  for (int t = u.first; t < total; t += u.step) {
+    const Tile tl = own_rows<CG>(next, u.rank);
+    next = tile_ahead<CG>(p, t + u.step, total);
     const int rows = min(32, tl.rows - 32 * quarter);
     if (!warp_wait(smem_u32(&s.tfull), phase, &s.abort_flag, p.status)) return;
     fence_after();
@@ -534,7 +620,10 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
     // the accumulator is in registers: the next tile's MMAs may start
     fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.tempty));
+    if (lane == 0) {
+      if (CG == 1) mbar_arrive(tempty);
+      else mbar_arrive_cluster(tempty);
+    }
     if constexpr (OUT == OUT_SITU) {
       bool ok;
       finish_situ(p, tl, v, rows, quarter, part, st, phase, s, ok);
@@ -546,39 +635,38 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
   }
 }
 
-template <int OUT>
-__global__ void __launch_bounds__(Cfg<OUT>::THREADS, 1) experts_fp8_kernel(const __grid_constant__ Params p) {
+template <int OUT, int CG>
+__global__ void __launch_bounds__(Cfg<OUT, CG>::THREADS, 1)
+    experts_fp8_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<OUT, CG>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync s;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t stage_base = ring + STAGES * STAGE_BYTES;
+  const uint32_t stage_base = ring + C::STAGES * C::STAGE_BYTES;
   const uint32_t sf = stage_base + EPI_BYTES;
   const int warp = threadIdx.x >> 5;
+  const Unit u = CG == 1 ? Unit{(int)blockIdx.x, (int)gridDim.x, 0}
+                         : Unit{(int)(blockIdx.x >> 1), (int)(gridDim.x >> 1), (int)cluster_rank()};
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1 + Cfg<OUT>::GATHER_WARPS);
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1 + CG * C::GATHER_WARPS);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < SF_STAGES; ++i) {
-      mbar_init(smem_u32(&s.sfull[i]), 1);
+      mbar_init(smem_u32(&s.sfull[i]), CG);
       mbar_init(smem_u32(&s.sempty[i]), 1);
     }
     mbar_init(smem_u32(&s.tfull), 1);
-    mbar_init(smem_u32(&s.tempty), Cfg<OUT>::EPI_WARPS);
+    mbar_init(smem_u32(&s.tempty), CG * C::EPI_WARPS);
     mbar_init(smem_u32(&s.drain), 1);
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.quarter[i]), Cfg<OUT>::SPLIT);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.quarter[i]), C::SPLIT);
     s.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&s.tmem)),
-                 "r"(TMEM_COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tmem_alloc<CG>(smem_u32(&s.tmem), TMEM_COLS);
   fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();  // both CTAs' barriers exist before any remote arrive
   fence_after();
   const uint32_t tmem = s.tmem;
   // everything above overlaps the previous kernel; inputs are read only below
@@ -588,26 +676,25 @@ __global__ void __launch_bounds__(Cfg<OUT>::THREADS, 1) experts_fp8_kernel(const
   if (warp < EPI_WARP0) {
     if (OUT == OUT_SITU) regs_dec<REGS_OTHER>();
     if (warp == 0) {
-      if ((threadIdx.x & 31) == 0) produce<OUT>(p, ring, s);
+      if ((threadIdx.x & 31) == 0) produce<OUT, CG>(p, ring, s, u);
     } else if (warp == 1) {
-      if ((threadIdx.x & 31) == 0) issue_mmas<OUT>(p, ring, sf, tmem, s);
+      if (u.rank == 0) issue_mmas<OUT, CG>(p, ring, sf, tmem, s, u);
     } else if (warp == 2) {
-      produce_scales<OUT>(p, sf, s);
+      produce_scales<OUT, CG>(p, sf, s, u);
     }
-  } else if (warp < Cfg<OUT>::GATHER_WARP0) {
+  } else if (warp < C::GATHER_WARP0) {
     if (OUT == OUT_SITU) regs_inc<REGS_EPI>();
-    epilogue<OUT>(p, tmem, stage_base, s);
+    epilogue<OUT, CG>(p, tmem, stage_base, s, u);
   } else if (OUT == OUT_SITU) {
     regs_dec<REGS_OTHER>();
-    gather_rows(p, ring, s);
+    gather_rows<CG>(p, ring, s, u);
   }
 
   fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();  // neither CTA frees TMEM or exits while its pair still works
   fence_after();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
-                 : "memory");
+  if (warp == 1) tmem_free<CG>(tmem, TMEM_COLS);
 }
 
 // ------------------------------------------------------------ host side
@@ -654,8 +741,9 @@ struct Device {
   int sms;
 };
 
-template <int OUT>
+template <int OUT, int CG>
 cudaError_t launch(const Params& p, int64_t max_tiles, cudaStream_t st) {
+  using C = Cfg<OUT, CG>;
   static Device devs[kMaxDevices];
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -667,18 +755,22 @@ cudaError_t launch(const Params& p, int64_t max_tiles, cudaStream_t st) {
     if (d.sms == 0) {
       e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
       if (e != cudaSuccess) return e;
-      e = cudaFuncSetAttribute(experts_fp8_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SMEM_BYTES);
+      e = cudaFuncSetAttribute(experts_fp8_kernel<OUT, CG>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
       if (e != cudaSuccess) return e;
       d.sms = sms;
     }
     sms = d.sms;
   }
-  const int grid = (int)std::min<int64_t>(max_tiles * p.n_tiles, sms);
-  if (grid <= 0) return cudaSuccess;
+  const int units = (int)std::min<int64_t>(max_tiles * p.n_tiles, sms / CG);
+  if (units <= 0) return cudaSuccess;
   count_launch();
-  return launch_pdl(experts_fp8_kernel<OUT>, dim3(grid), dim3(Cfg<OUT>::THREADS), (size_t)SMEM_BYTES, st, 1,
-                    p);
+  return launch_pdl(experts_fp8_kernel<OUT, CG>, dim3(CG * units), dim3(C::THREADS),
+                    (size_t)C::SMEM_BYTES, st, CG, p);
+}
+template <int OUT>
+cudaError_t launch(const Params& p, bool pairs, int64_t max_tiles, cudaStream_t st) {
+  return pairs ? launch<OUT, 2>(p, max_tiles, st) : launch<OUT, 1>(p, max_tiles, st);
 }
 
 }  // namespace
@@ -712,9 +804,11 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st) 
   p.beta1 = g.beta1;
   p.beta2 = g.beta2;
   p.n_tiles = g.situ ? p.w_blocks : (g.n_out + 2 * SUB - 1) / (2 * SUB);
-  const int64_t max_tiles = g.tiles != nullptr ? g.max_tiles : (g.rows + BM - 1) / BM;
-  if (g.situ) return launch<OUT_SITU>(p, max_tiles, st);
-  return g.out_f32 ? launch<OUT_F32>(p, max_tiles, st) : launch<OUT_BF16>(p, max_tiles, st);
+  const int tile_m = g.pairs ? 2 * BM : BM;
+  const int64_t max_tiles = g.tiles != nullptr ? g.max_tiles : (g.rows + tile_m - 1) / tile_m;
+  if (g.situ) return launch<OUT_SITU>(p, g.pairs, max_tiles, st);
+  return g.out_f32 ? launch<OUT_F32>(p, g.pairs, max_tiles, st)
+                   : launch<OUT_BF16>(p, g.pairs, max_tiles, st);
 }
 
 }  // namespace lmoe

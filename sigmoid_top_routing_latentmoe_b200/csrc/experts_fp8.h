@@ -13,13 +13,13 @@ constexpr int kQBlock = 128;
 inline int q_words(int64_t cols) { return (int)((cols + 511) / 512); }
 inline int q_blocks(int64_t n) { return (int)((n + kQBlock - 1) / kQBlock); }
 
-// Tile list of a ragged product, written by the first block of the quantiser
-// of the rows or by launch_expert_tiles: (expert, first row, rows) of at most
-// kTileM rows.
+// Tile list of a ragged product (launch_expert_tiles): (expert, first row, rows) of at most
+// tile_m rows.
 struct TileList {
   const int32_t* offsets;  // [R + 1], clamped to [0, rows]
   int R;
   int64_t rows;
+  int tile_m;    // kTileM or kRoutedPairTileM
   int max_tiles;
   int32_t* n_mtiles;
   int4* tiles;
@@ -63,6 +63,9 @@ struct Fp8Gemm {
   const int4* tiles;        // nullptr: one expert that has every row
   const int32_t* n_mtiles;
   int max_tiles;
+  // CTA pairs over tiles of 256 rows, else single CTAs over tiles of 128; the
+  // tile list has to be of that height.
+  bool pairs;
 };
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st);
 

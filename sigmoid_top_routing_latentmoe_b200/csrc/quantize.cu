@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const T* __restri
 }
 
 // The tile list of a ragged product: expert e's rows [offsets[e], offsets[e + 1])
-// in tiles of at most kTileM.  Offsets are clamped to an ascending order inside
+// in tiles of at most tile_m.  Offsets are clamped to an ascending order inside
 // [0, rows] and the list to max_tiles, so that no list leads a product out of
 // its buffers.  One block; a block-wide scan over 1024 experts at a time.
 __global__ void __launch_bounds__(1024) expert_tiles_kernel(TileList t) {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(1024) expert_tiles_kernel(TileList t) {
       lo = (int)min((int64_t)max(t.offsets[e], 0), t.rows);
       hi = (int)min((int64_t)max(t.offsets[e + 1], lo), t.rows);
     }
-    const int n = (hi - lo + kTileM - 1) / kTileM;
+    const int n = (hi - lo + t.tile_m - 1) / t.tile_m;
     int inc = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(1024) expert_tiles_kernel(TileList t) {
     int at = base + before + inc - n;
     for (int j = 0; j < n; ++j, ++at)
       if (at < t.max_tiles)
-        t.tiles[at] = make_int4(e, lo + j * kTileM, min(kTileM, hi - lo - j * kTileM), 0);
+        t.tiles[at] = make_int4(e, lo + j * t.tile_m, min(t.tile_m, hi - lo - j * t.tile_m), 0);
     base += total;
     __syncthreads();
   }
