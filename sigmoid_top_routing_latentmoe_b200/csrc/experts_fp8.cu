@@ -8,13 +8,11 @@
 // One persistent, warp-specialised kernel; a tile is 128 rows of one expert (256
 // on a CTA pair) x 256 columns (SiTU: 128 gate and the 128 matching up columns), K in blocks of
 // 128 (one 128-byte swizzle row):
-//   warp 0     TMA producer: A rows and two 128-row B boxes per K block,
-//   warp 1     MMA issuer and TMEM allocator; every fourth K block it also
-//              copies the next four blocks' scale words to TMEM,
-//   warp 2     scale producer: the words of four K blocks (128 rows of A, one
-//              or two weight blocks) in the order tcgen05.cp wants,
-//   warps 4-   epilogue, two (SiTU: four) per 32-row quarter, sharing its columns,
-//   then, SiTU only, four warps that copy the rows of A that p.index names.
+//   warp 0      TMA producer: A rows and two 128-row B boxes per K block,
+//   warp 1      MMA issuer and TMEM allocator,
+//   warps 4-19  epilogue, four per 32-row quarter, sharing its columns,
+//   warps 20-23 the scale words of four K blocks at a time, written to TMEM;
+//               SiTU: also the rows of A that p.index names.
 #include <cuda.h>
 
 #include <algorithm>
@@ -36,38 +34,33 @@ constexpr int BM = 128, SUB = 128, BK = 128;
 constexpr int A_BYTES = BM * BK, SUB_BYTES = SUB * BK;
 constexpr int SMALL_ROWS = 32;            // tiles of at most this many rows load a smaller A box
 constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
-constexpr int SF_BYTES = 3 * 512;         // A words, then two blocks of B words
 constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
 constexpr int TMEM_COLS = 512, SF_COL0 = 256;
-constexpr int EPI_WARP0 = 4;
-constexpr int EPI_BYTES = 8 * 32 * 64;    // staging of all epilogue warps
 static_assert(SF_COL0 + SF_STAGES * SF_COLS <= TMEM_COLS, "TMEM");
+constexpr int EPI_WARP0 = 4, EPI_WARPS = 16, ROW_WARP0 = EPI_WARP0 + EPI_WARPS, ROW_WARPS = 4;
+constexpr int THREADS = 32 * (ROW_WARP0 + ROW_WARPS);
+// Staging bytes of an epilogue warp.  SiTU stages 32 rows x 32 bytes, in the
+// first half; the second holds the rows' maxima (tile parity, warp of the
+// quarter, quarter and row).
+constexpr int EPI_STAGE = 32 * 64;
+constexpr int SITU_STAGE = 32 * 32, AMAX_BYTES = 2 * 4 * 128 * 4;
+static_assert(SITU_STAGE * EPI_WARPS + AMAX_BYTES <= EPI_STAGE * EPI_WARPS, "staging");
+// The 768 threads start with 80 registers each; the 16 epilogue warps hold 64
+// accumulators a thread and take what the other 8 give up (512 x 96 + 256 x 48
+// = 768 x 80).
+constexpr int REGS_EPI = 96, REGS_OTHER = 48;
 enum Out { OUT_BF16 = 0, OUT_F32 = 1, OUT_SITU = 2 };
 
 // CG = 1: a CTA computes a 128-row tile and loads both B boxes of a K block.
 // CG = 2: a CTA pair (cluster of 2) computes a 256-row tile; each CTA loads its
 //   own 128 rows of A, one of the two B boxes and its own scale words, and the
 //   leader (rank 0) issues the MMAs of both.
-// Epilogue warps share a 32-row quarter of a CTA's rows by columns.  Plain tiles:
-// 2 warps with 128 columns each; SiTU tiles: 4 warps with 32 hidden units each,
-// whose 64 accumulators leave the compiler room to overlap the units.
-template <int OUT, int CG>
+template <int CG>
 struct Cfg {
   static constexpr int STAGE_BYTES = A_BYTES + (CG == 1 ? 2 : 1) * SUB_BYTES;
   static constexpr int STAGES = CG == 1 ? 4 : 6;
-  static constexpr int SPLIT = OUT == OUT_SITU ? 4 : 2;   // epilogue warps per quarter
-  static constexpr int EPI_WARPS = 4 * SPLIT;
-  static constexpr int EPI_STAGE = 32 * (OUT == OUT_SITU ? 32 : 64);  // bytes per warp
-  static constexpr int GATHER_WARP0 = EPI_WARP0 + EPI_WARPS;
-  static constexpr int GATHER_WARPS = OUT == OUT_SITU ? 4 : 0;
-  static constexpr int THREADS = 32 * (GATHER_WARP0 + GATHER_WARPS);
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + SF_STAGES * SF_BYTES + 1024;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * EPI_STAGE + 1024;
 };
-static_assert(Cfg<OUT_SITU, 1>::SMEM_BYTES + 5 * 1024 <= 232448, "shared memory");
-static_assert(Cfg<OUT_SITU, 2>::SMEM_BYTES + 5 * 1024 <= 232448, "shared memory");
-// The SiTU kernel's 768 threads start with 80 registers each; its 16 epilogue
-// warps take what the other 8 give up (512 x 96 + 256 x 48 = 768 x 80).
-constexpr int REGS_EPI = 96, REGS_OTHER = 48;
 
 struct Params {
   CUtensorMap tmA, tmA32, tmB0, tmB1;
@@ -125,16 +118,17 @@ __device__ __forceinline__ bool two_subs(const Params& p, const Tile& tl) {
 
 struct Sync {
   uint64_t full[6], empty[6], sfull[SF_STAGES], sempty[SF_STAGES], tfull, tempty, drain, quarter[4];
-  float amax[2][4][4][32];  // tile parity, quarter, warp of the quarter, row
   uint32_t tmem;
   volatile int abort_flag;
 };
+static_assert(Cfg<1>::SMEM_BYTES + sizeof(Sync) <= 232448 &&
+                  Cfg<2>::SMEM_BYTES + sizeof(Sync) <= 232448, "shared memory");
 
 // The SiTU product takes its rows of A through p.index (gather_rows), the
 // others their neighbouring rows by TMA.
 template <int OUT, int CG>
 __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
-  using C = Cfg<OUT, CG>;
+  using C = Cfg<CG>;
   constexpr bool GATHER = OUT == OUT_SITU;
   int stage = 0;
   uint32_t phase = 0, issued = 0, issued_phase = 0;
@@ -186,94 +180,8 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
       }
 }
 
-// Rows of A by index, four warps with 32 rows each, by 16-byte asynchronous
-// copies into the swizzled layout a TMA load would leave.  A stage is
-// announced once its copies have landed; up to IN_FLIGHT stages stay in
-// flight, but none while the ring is full, when the tensor cores may be
-// waiting for exactly these.  Every copy reads inside its row, so that none
-// needs zero-filling (whose branches took longer): columns past n_in repeat
-// the last ones (they meet zeros of W), rows past the tile repeat its last row
-// (never stored), and an index outside A reads row 0 (its scale words are 0,
-// and so is its product).
-constexpr int IN_FLIGHT = 2;
-__device__ __forceinline__ void load_index(const Params& p, const Tile& tl, int row0, int (&row)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = min(row0 + 4 * i, tl.rows - 1);
-    row[i] = r >= 0 ? p.index[tl.m0 + r] : 0;
-    if ((uint32_t)row[i] >= (uint32_t)p.a_rows) row[i] = 0;
-  }
-}
-template <int CG>
-__device__ void gather_rows(const Params& p, uint32_t ring, Sync& s, Unit u) {
-  using C = Cfg<OUT_SITU, CG>;
-  const int lane = threadIdx.x & 31, first = 32 * ((threadIdx.x >> 5) & 3);
-  const int chunk = lane & 7, row0 = first + (lane >> 3);
-  int stage = 0, head = 0;  // next stage to fill, oldest stage in flight
-  int flying = 0;
-  uint32_t phase = 0;
-  const int total = total_tiles<CG>(p);
-  const uint32_t lead0 = CG == 1 ? smem_u32(s.full) : map_to_rank(smem_u32(s.full), 0);
-  auto announce = [&]() {  // the oldest stage in flight, once it has landed
-    if (flying == 1) cp_async_wait<0>();
-    else if (flying == 2) cp_async_wait<1>();
-    else cp_async_wait<2>();
-    fence_async_smem<CG>();
-    __syncwarp();
-    if (lane == 0) {
-      if (CG == 1) mbar_arrive(lead0 + 8 * head);
-      else mbar_arrive_cluster(lead0 + 8 * head);
-    }
-    if (++head == C::STAGES) head = 0;
-    --flying;
-  };
-  int row[8];  // of the next tile
-  Tile tl = own_rows<CG>(tile_ahead<CG>(p, u.first, total), u.rank);
-  Tile tn = own_rows<CG>(tile_ahead<CG>(p, u.first + u.step, total), u.rank);
-  load_index(p, tl, row0, row);
-  for (int t = u.first; t < total; t += u.step) {
-    const uint8_t* at[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) at[i] = p.a + (int64_t)row[i] * p.n_in;
-    load_index(p, tn, row0, row);
-    const Tile after = own_rows<CG>(tile_ahead<CG>(p, t + 2 * u.step, total), u.rank);
-    for (int kb = 0; kb < p.kb; ++kb) {
-      const uint32_t empty = smem_u32(&s.empty[stage]);
-      while (flying > 0 && (flying > IN_FLIGHT ||
-                            !__all_sync(0xffffffffu, mbar_try_wait(empty, phase ^ 1u))))
-        announce();
-      if (!warp_wait(empty, phase ^ 1u, &s.abort_flag, p.status)) {
-        cp_async_wait<0>();
-        return;
-      }
-      const uint32_t dst = ring + stage * C::STAGE_BYTES + row0 * BK;
-      const int col = min(kb * BK + chunk * 16, p.n_in - 16);
-      // row0 + 4 i: its last three bits alternate between two values
-      const uint32_t dst0 = dst + ((chunk ^ (row0 & 7)) << 4);
-      const uint32_t dst1 = dst + 4 * BK + ((chunk ^ ((row0 + 4) & 7)) << 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (first + 4 * i < tl.rows)
-          cp_async16((i & 1 ? dst1 : dst0) + (i >> 1) * 8 * BK, at[i] + col);
-      cp_async_commit();
-      ++flying;
-      if (++stage == C::STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    tl = tn;
-    tn = after;
-  }
-  while (flying > 0) announce();
-}
-
-// Scale words of four K blocks: row r of A at byte (r % 32) * 16 + (r / 32) * 4,
-// so that tcgen05.cp puts it in lane r % 32, column r / 32; a weight block has
-// one word for its 128 rows.  Each CTA of a pair prepares its own rows' words
-// and those of both weight blocks.  The words are loaded one step ahead, a
-// tile's row numbers one tile ahead: loaded when needed, they held the tensor
-// cores up (450 instead of 400 ns a K block on single CTAs, 437 / 374 on pairs).
+// Scale words of four K blocks of a tile: of 128 rows of A, four per lane (rows
+// lane + 32 j), and of the two weight blocks.
 struct ScaleRows {
   int row[4];                // rows of A, -1: none (its product is not stored, or of zeros)
   const uint32_t *w0, *w1;   // words of the two weight blocks
@@ -282,11 +190,9 @@ struct ScaleWords {
   uint32_t a[4], b0, b1;
 };
 template <int OUT, int CG>
-__device__ __forceinline__ ScaleRows scale_rows(const Params& p, int t, int total, const Unit& u) {
+__device__ __forceinline__ ScaleRows scale_rows(const Params& p, const Tile& tl) {
   const int lane = threadIdx.x & 31;
   ScaleRows r{{-1, -1, -1, -1}, nullptr, nullptr};
-  if (t >= total) return r;
-  const Tile tl = own_rows<CG>(decode_tile<CG>(p, t), u.rank);
   const int nb0 = OUT == OUT_SITU ? tl.n : 2 * tl.n;
   const int64_t at = ((int64_t)tl.e * p.w_blocks + nb0) * p.words;
   r.w0 = p.w_words + at;
@@ -301,7 +207,6 @@ __device__ __forceinline__ ScaleRows scale_rows(const Params& p, int t, int tota
 }
 __device__ __forceinline__ ScaleWords scale_words(const Params& p, const ScaleRows& r, int q) {
   ScaleWords w{{0, 0, 0, 0}, 0, 0};
-  if (r.w0 == nullptr) return w;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (r.row[j] >= 0) w.a[j] = p.a_words[(int64_t)q * p.a_rows + r.row[j]];
@@ -309,49 +214,148 @@ __device__ __forceinline__ ScaleWords scale_words(const Params& p, const ScaleRo
   w.b1 = r.w1[q];
   return w;
 }
+
+// Rows of A by index (SiTU), 32 per warp: 16-byte asynchronous copies into the
+// swizzled layout a TMA load would leave.  Every copy reads inside its row, so
+// that none needs zero-filling (whose branches took longer): columns past n_in
+// repeat the last ones (they meet zeros of W), rows past the tile repeat its
+// last row (never stored), and an index outside A reads row 0 (its scale words
+// are 0, and so is its product).
+__device__ __forceinline__ void load_index(const Params& p, const Tile& tl, int row0, int (&row)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = min(row0 + 4 * i, tl.rows - 1);
+    row[i] = r >= 0 ? p.index[tl.m0 + r] : 0;
+    if ((uint32_t)row[i] >= (uint32_t)p.a_rows) row[i] = 0;
+  }
+}
+
+// The four row warps.  Scales: warp w writes the words to TMEM lanes 32 w ...:
+// columns 0-3 the words of rows 0-31, 32-63, 64-95 and 96-127 of A, 4-7 and
+// 8-11 those of the two weight blocks (one word for their 128 rows), the same in
+// each quarter, as the block-scaled MMA reads them.  Words, row numbers and
+// tiles are loaded one step ahead.
+// SiTU: a stage of A is announced once its copies have landed; up to IN_FLIGHT
+// stages stay in flight, but none while the ring is full, when the tensor cores
+// may be waiting for exactly these.
+constexpr int IN_FLIGHT = 2;
 template <int OUT, int CG>
-__device__ void produce_scales(const Params& p, uint32_t sf, Sync& s, Unit u) {
-  const int lane = threadIdx.x & 31;
+__device__ void feed_rows(const Params& p, uint32_t ring, uint32_t tmem, Sync& s, Unit u) {
+  using C = Cfg<CG>;
+  constexpr bool GATHER = OUT == OUT_SITU;
+  const int lane = threadIdx.x & 31, first = 32 * ((threadIdx.x >> 5) & 3);
+  const int chunk = lane & 7, row0 = first + (lane >> 3);
+  const int total = total_tiles<CG>(p);
+  const uint32_t sfull0 = CG == 1 ? smem_u32(s.sfull) : map_to_rank(smem_u32(s.sfull), 0);
+  const uint32_t full0 = smem_u32(s.full), sf0 = tmem + SF_COL0 + ((uint32_t)first << 16);
+  int sstage = 0, stage = 0, head = 0;  // next scale stage, next stage, oldest stage in flight
+  uint32_t sphase = 0, phase = 0;
+  int flying = 0;
+  auto announce = [&]() {  // the oldest stage in flight, once it has landed
+    if (flying == 1) cp_async_wait<0>();
+    else if (flying == 2) cp_async_wait<1>();
+    else cp_async_wait<2>();
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full0 + 8 * head);  // a pair's second CTA relays it to the leader
+    if (++head == C::STAGES) head = 0;
+    --flying;
+  };
+  Tile tl = own_rows<CG>(tile_ahead<CG>(p, u.first, total), u.rank);
+  Tile tn = own_rows<CG>(tile_ahead<CG>(p, u.first + u.step, total), u.rank);
+  int row[8];  // GATHER: of the next tile
+  if (GATHER) load_index(p, tl, row0, row);
+  ScaleRows rows = scale_rows<OUT, CG>(p, tl);
+  ScaleWords next = scale_words(p, rows, 0);
+  bool ok = true;
+  for (int t = u.first; ok && t < total; t += u.step) {
+    const uint8_t* at[8];
+    if (GATHER) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) at[i] = p.a + (int64_t)row[i] * p.n_in;
+      load_index(p, tn, row0, row);
+    }
+    const ScaleRows rows1 = scale_rows<OUT, CG>(p, tn);
+    const Tile after = own_rows<CG>(tile_ahead<CG>(p, t + 2 * u.step, total), u.rank);
+    for (int kb = 0; kb < p.kb; kb += GATHER ? 1 : 4) {
+      if (!GATHER || (kb & 3) == 0) {
+        const ScaleWords w = next;
+        const int q = (kb >> 2) + 1;
+        next = q < p.words ? scale_words(p, rows, q) : scale_words(p, rows1, 0);
+        ok = warp_wait(smem_u32(&s.sempty[sstage]), sphase ^ 1u, &s.abort_flag, p.status);
+        if (!ok) break;
+        fence_after();
+        const uint32_t v[16] = {w.a[0], w.a[1], w.a[2], w.a[3], w.b0, w.b0, w.b0, w.b0,
+                                w.b1,   w.b1,   w.b1,   w.b1,   0,    0,    0,    0};
+        st16(sf0 + sstage * SF_COLS, v);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 1) mbar_arrive(sfull0 + 8 * sstage);
+          else mbar_arrive_remote(sfull0 + 8 * sstage);
+        }
+        if (++sstage == SF_STAGES) {
+          sstage = 0;
+          sphase ^= 1u;
+        }
+      }
+      if (GATHER) {
+        const uint32_t empty = smem_u32(&s.empty[stage]);
+        while (flying > 0 && (flying > IN_FLIGHT ||
+                              !__all_sync(0xffffffffu, mbar_try_wait(empty, phase ^ 1u))))
+          announce();
+        ok = warp_wait(empty, phase ^ 1u, &s.abort_flag, p.status);
+        if (!ok) break;
+        const uint32_t dst = ring + stage * C::STAGE_BYTES + row0 * BK;
+        const int col = min(kb * BK + chunk * 16, p.n_in - 16);
+        // row0 + 4 i: its last three bits alternate between two values
+        const uint32_t dst0 = dst + ((chunk ^ (row0 & 7)) << 4);
+        const uint32_t dst1 = dst + 4 * BK + ((chunk ^ ((row0 + 4) & 7)) << 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (first + 4 * i < tl.rows)
+            cp_async16((i & 1 ? dst1 : dst0) + (i >> 1) * 8 * BK, at[i] + col);
+        cp_async_commit();
+        ++flying;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    rows = rows1;
+    tl = tn;
+    tn = after;
+  }
+  if (!ok) cp_async_wait<0>();
+  while (ok && flying > 0) announce();
+}
+
+// The second CTA of a pair passes the landed stages of its rows on to the
+// leader's barriers.
+template <int CG>
+__device__ void relay_rows(const Params& p, Sync& s, Unit u) {
+  const int total = total_tiles<CG>(p);
+  const uint32_t lead0 = map_to_rank(smem_u32(s.full), 0);
   int stage = 0;
   uint32_t phase = 0;
-  const int total = total_tiles<CG>(p);
-  const uint32_t lead0 = CG == 1 ? smem_u32(s.sfull) : map_to_rank(smem_u32(s.sfull), 0);
-  ScaleRows rows = scale_rows<OUT, CG>(p, u.first, total, u);
-  ScaleWords next = scale_words(p, rows, 0);
-  for (int t = u.first; t < total; t += u.step) {
-    const ScaleRows rows1 = scale_rows<OUT, CG>(p, t + u.step, total, u);
-    for (int q = 0; q < p.words; ++q) {
-      const ScaleWords w = next;
-      next = q + 1 < p.words ? scale_words(p, rows, q + 1) : scale_words(p, rows1, 0);
-      if (!warp_wait(smem_u32(&s.sempty[stage]), phase ^ 1u, &s.abort_flag, p.status)) return;
-      const uint32_t dst = sf + stage * SF_BYTES + lane * 16;
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.a[0]), "r"(w.a[1]),
-                   "r"(w.a[2]), "r"(w.a[3])
-                   : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + 512), "r"(w.b0) : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + 1024), "r"(w.b1) : "memory");
-      fence_async_smem<CG>();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 1) mbar_arrive(lead0 + 8 * stage);
-        else mbar_arrive_cluster(lead0 + 8 * stage);
-      }
-      if (++stage == SF_STAGES) {
+  for (int t = u.first; t < total; t += u.step)
+    for (int kb = 0; kb < p.kb; ++kb) {
+      if (!mbar_wait(smem_u32(&s.full[stage]), phase, &s.abort_flag, p.status)) return;
+      mbar_arrive_remote(lead0 + 8 * stage);
+      if (++stage == Cfg<CG>::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
-    rows = rows1;
-  }
 }
 
 // The whole warp walks the tiles, so that addresses and descriptors stay in
 // uniform registers, and one elected lane issues (a single lane walking alone
 // took about 700 cycles a K block to issue what the tensor cores do in 512).
 template <int OUT, int CG>
-__device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t sf, uint32_t tmem, Sync& s,
-                           Unit u) {
-  using C = Cfg<OUT, CG>;
+__device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t tmem, Sync& s, Unit u) {
+  using C = Cfg<CG>;
   constexpr bool PAIR = CG == 2;
   int stage = 0, sstage = 0;
   uint32_t phase = 0, sphase = 0, tphase = 0;
@@ -373,12 +377,6 @@ __device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t sf, uint32_t
           break;
         }
         fence_after();
-        const uint64_t src = desc_scales(sf + sstage * SF_BYTES);
-        if (elect_one()) {
-          cp_scales<CG>(sfa, src);
-          cp_scales<CG>(sfb, src + (512 >> 4));
-          if (two) cp_scales<CG>(sfb + 4, src + (1024 >> 4));
-        }
       }
       if (!warp_wait<PAIR>(smem_u32(&s.full[stage]), phase, &s.abort_flag, p.status)) {
         ok = false;
@@ -515,9 +513,10 @@ __device__ __forceinline__ float situ_unit(float a, float c, float b1, float b2,
 // A tile's hidden units of this warp: 32 rows x 32 units, quantised with the
 // maximum over the row's 128.
 __device__ __forceinline__ void finish_situ(const Params& p, const Tile& tl, float (&v)[64], int rows,
-                                            int quarter, int part, uint32_t st, uint32_t phase,
-                                            Sync& s, bool& ok) {
+                                            int quarter, int part, uint32_t st, float* amax,
+                                            uint32_t phase, Sync& s, bool& ok) {
   const int lane = threadIdx.x & 31;
+  amax += phase * 512 + 32 * quarter + lane;  // of this row: [part * 128]
   float m = 0.0f;
   if (rows > 0) {
     float ma = 0.0f, mc = 0.0f;
@@ -539,13 +538,13 @@ __device__ __forceinline__ void finish_situ(const Params& p, const Tile& tl, flo
 #pragma unroll
     for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));  // finite, or NaN: left out
   }
-  s.amax[phase][quarter][part][lane] = m;
+  amax[128 * part] = m;
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&s.quarter[quarter]));
   ok = warp_wait(smem_u32(&s.quarter[quarter]), phase, &s.abort_flag, p.status);
   if (!ok || rows <= 0) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, s.amax[phase][quarter][i][lane]);
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, amax[128 * i]);
   const int e = scale_exponent(m);
   const float inv = pow2_f(-e);
   uint32_t w[8];
@@ -562,16 +561,16 @@ __device__ __forceinline__ void finish_situ(const Params& p, const Tile& tl, flo
     p.out_scales[((int64_t)(tl.n >> 2) * p.rows + row0 + lane) * 4 + (tl.n & 3)] = (uint8_t)(e + 127);
 }
 
-// A plain tile's 32 rows x 128 columns of this warp.
+// A plain tile's 32 rows x 64 columns of this warp.
 template <int OUT>
-__device__ __forceinline__ void finish_store(const Params& p, const Tile& tl, const float (&v)[128],
+__device__ __forceinline__ void finish_store(const Params& p, const Tile& tl, const float (&v)[64],
                                              int rows, int quarter, int part, uint32_t st) {
   constexpr int ES = OUT == OUT_F32 ? 4 : 2, CB = 64 / ES;  // columns of a 64-byte block
   const int64_t ld = (int64_t)p.n_out * ES;
   char* base = static_cast<char*>(p.out) + (int64_t)(tl.m0 + 32 * quarter) * ld;
 #pragma unroll
-  for (int b = 0; b < SUB / CB; ++b) {
-    const int col = tl.n * 2 * SUB + SUB * part + b * CB;
+  for (int b = 0; b < 64 / CB; ++b) {
+    const int col = tl.n * 2 * SUB + 64 * part + b * CB;
     if (rows > 0 && col < p.n_out) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -589,11 +588,11 @@ __device__ __forceinline__ void finish_store(const Params& p, const Tile& tl, co
 }
 
 template <int OUT, int CG>
-__device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sync& s, Unit u) {
-  using C = Cfg<OUT, CG>;
+__device__ void epilogue(const Params& p, uint32_t tmem, uint8_t* staging, Sync& s, Unit u) {
   const int lane = threadIdx.x & 31, ew = (threadIdx.x >> 5) - EPI_WARP0;
   const int quarter = ew & 3, part = ew >> 2;  // TMEM lanes 32 (warp mod 4) ..., columns
-  const uint32_t st = stage_base + ew * C::EPI_STAGE;
+  const uint32_t st = smem_u32(staging) + ew * (OUT == OUT_SITU ? SITU_STAGE : EPI_STAGE);
+  float* amax = reinterpret_cast<float*>(staging + EPI_WARPS * SITU_STAGE);
   const uint32_t ta = tmem + ((uint32_t)(32 * quarter) << 16);
   // the leader's MMA thread waits for the epilogues of both CTAs
   const uint32_t tempty = CG == 1 ? smem_u32(&s.tempty) : map_to_rank(smem_u32(&s.tempty), 0);
@@ -606,15 +605,10 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
     const int rows = min(32, tl.rows - 32 * quarter);
     if (!warp_wait(smem_u32(&s.tfull), phase, &s.abort_flag, p.status)) return;
     fence_after();
-    float v[OUT == OUT_SITU ? 64 : 128];
-    if (rows > 0) {
-      if (OUT == OUT_SITU) {
-        ld32(ta + 32 * part, v);
-        ld32(ta + SUB + 32 * part, v + 32);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ld32(ta + SUB * part + 32 * i, v + 32 * i);
-      }
+    float v[64];
+    if (rows > 0) {  // SiTU: 32 gate and the matching 32 up columns
+      ld32(ta + (OUT == OUT_SITU ? 32 : 64) * part, v);
+      ld32(ta + (OUT == OUT_SITU ? SUB + 32 * part : 64 * part + 32), v + 32);
       ld_wait();
     }
     // the accumulator is in registers: the next tile's MMAs may start
@@ -622,11 +616,11 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
     __syncwarp();
     if (lane == 0) {
       if (CG == 1) mbar_arrive(tempty);
-      else mbar_arrive_cluster(tempty);
+      else mbar_arrive_remote(tempty);
     }
     if constexpr (OUT == OUT_SITU) {
       bool ok;
-      finish_situ(p, tl, v, rows, quarter, part, st, phase, s, ok);
+      finish_situ(p, tl, v, rows, quarter, part, st, amax, phase, s, ok);
       if (!ok) return;
     } else {
       finish_store<OUT>(p, tl, v, rows, quarter, part, st);
@@ -636,30 +630,32 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint32_t stage_base, Sy
 }
 
 template <int OUT, int CG>
-__global__ void __launch_bounds__(Cfg<OUT, CG>::THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
     experts_fp8_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<OUT, CG>;
+  using C = Cfg<CG>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync s;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t stage_base = ring + C::STAGES * C::STAGE_BYTES;
-  const uint32_t sf = stage_base + EPI_BYTES;
+  uint8_t* staging = smem_raw + (ring - smem_u32(smem_raw)) + C::STAGES * C::STAGE_BYTES;
   const int warp = threadIdx.x >> 5;
   const Unit u = CG == 1 ? Unit{(int)blockIdx.x, (int)gridDim.x, 0}
                          : Unit{(int)(blockIdx.x >> 1), (int)(gridDim.x >> 1), (int)cluster_rank()};
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1 + CG * C::GATHER_WARPS);
+      // the producer's bytes, and SiTU the row warps (of a pair's second CTA
+      // through its own barriers, which only they use, and the relay)
+      mbar_init(smem_u32(&s.full[i]),
+                OUT != OUT_SITU ? 1 : u.rank == 1 ? ROW_WARPS : 1 + ROW_WARPS + (CG == 2 ? 1 : 0));
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < SF_STAGES; ++i) {
-      mbar_init(smem_u32(&s.sfull[i]), CG);
+      mbar_init(smem_u32(&s.sfull[i]), CG * ROW_WARPS);
       mbar_init(smem_u32(&s.sempty[i]), 1);
     }
     mbar_init(smem_u32(&s.tfull), 1);
-    mbar_init(smem_u32(&s.tempty), CG * C::EPI_WARPS);
+    mbar_init(smem_u32(&s.tempty), CG * EPI_WARPS);
     mbar_init(smem_u32(&s.drain), 1);
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.quarter[i]), C::SPLIT);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.quarter[i]), EPI_WARPS / 4);
     s.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -674,20 +670,19 @@ __global__ void __launch_bounds__(Cfg<OUT, CG>::THREADS, 1)
   pdl_wait();
 
   if (warp < EPI_WARP0) {
-    if (OUT == OUT_SITU) regs_dec<REGS_OTHER>();
+    regs_dec<REGS_OTHER>();
     if (warp == 0) {
       if ((threadIdx.x & 31) == 0) produce<OUT, CG>(p, ring, s, u);
     } else if (warp == 1) {
-      if (u.rank == 0) issue_mmas<OUT, CG>(p, ring, sf, tmem, s, u);
-    } else if (warp == 2) {
-      produce_scales<OUT, CG>(p, sf, s, u);
+      if (u.rank == 0) issue_mmas<OUT, CG>(p, ring, tmem, s, u);
+      else if (OUT == OUT_SITU && (threadIdx.x & 31) == 0) relay_rows<CG>(p, s, u);
     }
-  } else if (warp < C::GATHER_WARP0) {
-    if (OUT == OUT_SITU) regs_inc<REGS_EPI>();
-    epilogue<OUT, CG>(p, tmem, stage_base, s, u);
-  } else if (OUT == OUT_SITU) {
+  } else if (warp < ROW_WARP0) {
+    regs_inc<REGS_EPI>();
+    epilogue<OUT, CG>(p, tmem, staging, s, u);
+  } else {
     regs_dec<REGS_OTHER>();
-    gather_rows<CG>(p, ring, s, u);
+    feed_rows<OUT, CG>(p, ring, tmem, s, u);
   }
 
   fence_before();
@@ -743,7 +738,7 @@ struct Device {
 
 template <int OUT, int CG>
 cudaError_t launch(const Params& p, int64_t max_tiles, cudaStream_t st) {
-  using C = Cfg<OUT, CG>;
+  using C = Cfg<CG>;
   static Device devs[kMaxDevices];
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -765,7 +760,7 @@ cudaError_t launch(const Params& p, int64_t max_tiles, cudaStream_t st) {
   const int units = (int)std::min<int64_t>(max_tiles * p.n_tiles, sms / CG);
   if (units <= 0) return cudaSuccess;
   count_launch();
-  return launch_pdl(experts_fp8_kernel<OUT, CG>, dim3(CG * units), dim3(C::THREADS),
+  return launch_pdl(experts_fp8_kernel<OUT, CG>, dim3(CG * units), dim3(THREADS),
                     (size_t)C::SMEM_BYTES, st, CG, p);
 }
 template <int OUT>

@@ -105,8 +105,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
                    "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+// Arrives on the barrier at a cluster address, ordering no memory accesses of
+// its own: for what was read from or written to TMEM (ordered by
+// tcgen05.fence), or to shared memory and already visible to the async proxy.
+// (A release at cluster scope took some 1500 cycles.)
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
@@ -169,11 +173,9 @@ __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // Shared-memory writes of this thread become visible to the async proxy
-// (tcgen05 reads through it), CG = 2: of either CTA of the pair.
-template <int CG>
+// (tcgen05 reads through it).
 __device__ __forceinline__ void fence_async_smem() {
-  if (CG == 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  else asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 // Arrive, when this thread's MMAs are complete, on the barrier at this offset
 // (CG = 2: in both CTAs of the pair).
@@ -211,16 +213,6 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t adesc, uint64_t bd
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
-// 32 lanes x 128 bits of shared memory to 4 TMEM columns, repeated in the four
-// 32-lane quarters: row i of the 512 bytes (16 bytes) goes to lane i.  CG = 2:
-// in both CTAs, each from its own shared memory.
-template <int CG>
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
-  if (CG == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
   if (CG == 1) {
@@ -241,15 +233,11 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
 
-// Shared-memory matrix descriptors (version 1): K-major operand with 128-byte
-// swizzle, 8-row groups 1024 bytes apart; and unswizzled 8-row x 16-byte cores
-// 128 bytes apart (the scale words).
+// Shared-memory matrix descriptor (version 1): K-major operand with 128-byte
+// swizzle, 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
          (2ull << 61);
-}
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | (8ull << 16) | (8ull << 32) | (1ull << 46);
 }
 // Instruction descriptor of kind::mxf8f6f4: A and B e4m3, both K-major, E8M0
 // scales, M = 128 CG, N = n; the scale bytes' index is or-ed in (sf_id_bits).
@@ -278,6 +266,16 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 16 columns of this warp's 32 lanes, and the wait for them.
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
