@@ -336,11 +336,13 @@ static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* of
   return t;
 }
 
-// The rows of z quantised once, gate and up products (which gather each pair's
-// row) with the SiTU and the quantisation of the hidden units in their
-// epilogue, output product.  The quantised rows take the first half of the
-// workspace's sorted-row area (rows of 2 or 4 bytes an element) and their scales the
-// second; the hidden units likewise theirs.
+// The rows of z quantised, gate and up products with the SiTU and the
+// quantisation of the hidden units in their epilogue, output product.  On CTA
+// pairs the rows are quantised in sorted order; on single CTAs once per token,
+// and the products gather each pair's row (K3-width prompt batch: a sorted copy
+// is 470 MB to write and to read).  The quantised rows take the first half of
+// the workspace's sorted-row area (rows of 2 or 4 bytes an element) and their
+// scales the second; the hidden units likewise theirs.
 template <typename T>
 static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const int32_t* perm,
                                       const int32_t* offsets, const lmoe_fp8_experts* w, void* out,
@@ -350,25 +352,26 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   if (P == 0) return LMOE_OK;
   const int Lt = d->latent, F = d->ff_routed;
   uint8_t* zq = at<uint8_t>(ws, L.zp);
-  uint8_t* zs = zq + d->n_tokens * Lt;
+  uint8_t* zs = zq + P * Lt;
   uint8_t* hq = at<uint8_t>(ws, L.h);
   uint8_t* hs = hq + P * F;
   const TileList tl = tile_list(d, L, offsets, ws);
+  const bool pairs = tl.tile_m == kRoutedPairTileM;
   int32_t* status = &at<WsHeader>(ws, L.header)->status;
   {
     ProfScope ps("quantize", st);
     LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");
-    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, nullptr, d->n_tokens, Lt, zq,
-                                      zs, st),
+    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, pairs ? perm : nullptr,
+                                      pairs ? P : d->n_tokens, Lt, zq, zs, st),
               "quantize rows");
   }
   Fp8Gemm g{};
   g.rows = P; g.R = d->n_routed; g.tiles = tl.tiles; g.n_mtiles = tl.n_mtiles;
-  g.pairs = tl.tile_m == kRoutedPairTileM;
-  g.max_tiles = tl.max_tiles; g.beta1 = d->beta1; g.beta2 = d->beta2;
+  g.pairs = pairs; g.max_tiles = tl.max_tiles; g.beta1 = d->beta1; g.beta2 = d->beta2;
   {
     ProfScope ps("expert_gemm1", st);
-    g.a = zq; g.a_scales = zs; g.a_rows = d->n_tokens; g.index = perm; g.n_in = Lt; g.n_out = F; g.situ = 1;
+    g.a = zq; g.a_scales = zs; g.a_rows = pairs ? P : d->n_tokens;
+    g.index = pairs ? nullptr : perm; g.n_in = Lt; g.n_out = F; g.situ = 1;
     g.w = (const uint8_t*)w->w_g; g.w_scales = w->w_g_scales;
     g.w_up = (const uint8_t*)w->w_u; g.w_up_scales = w->w_u_scales;
     g.out = hq; g.out_scales = hs;

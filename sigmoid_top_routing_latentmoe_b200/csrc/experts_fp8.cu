@@ -12,7 +12,7 @@
 //   warp 1      MMA issuer and TMEM allocator,
 //   warps 4-19  epilogue, four per 32-row quarter, sharing its columns,
 //   warps 20-23 the scale words of four K blocks at a time, written to TMEM;
-//               SiTU: also the rows of A that p.index names.
+//               SiTU on single CTAs: also the rows of A that p.index names.
 #include <cuda.h>
 
 #include <algorithm>
@@ -47,7 +47,8 @@ constexpr int SITU_STAGE = 32 * 32, AMAX_BYTES = 2 * 4 * 128 * 4;
 static_assert(SITU_STAGE * EPI_WARPS + AMAX_BYTES <= EPI_STAGE * EPI_WARPS, "staging");
 // The 768 threads start with 80 registers each; the 16 epilogue warps hold 64
 // accumulators a thread and take what the other 8 give up (512 x 96 + 256 x 48
-// = 768 x 80).
+// = 768 x 80).  Shared memory leaves almost no L1, so a spilled register is read
+// back from L2: the roles are cut so that none spills in its loop.
 constexpr int REGS_EPI = 96, REGS_OTHER = 48;
 enum Out { OUT_BF16 = 0, OUT_F32 = 1, OUT_SITU = 2 };
 
@@ -77,6 +78,10 @@ struct Params {
   int32_t* status;
   float beta1, beta2;
 };
+
+// The gate and up products on single CTAs take their rows of A through p.index.
+template <int OUT, int CG>
+constexpr bool gathers() { return OUT == OUT_SITU && CG == 1; }
 
 // This CTA (or its pair): which of the tiles it takes, and its rank in the pair.
 struct Unit {
@@ -124,12 +129,11 @@ struct Sync {
 static_assert(Cfg<1>::SMEM_BYTES + sizeof(Sync) <= 232448 &&
                   Cfg<2>::SMEM_BYTES + sizeof(Sync) <= 232448, "shared memory");
 
-// The SiTU product takes its rows of A through p.index (gather_rows), the
-// others their neighbouring rows by TMA.
+// Neighbouring rows of A come by TMA, those named by p.index from the row warps.
 template <int OUT, int CG>
 __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
   using C = Cfg<CG>;
-  constexpr bool GATHER = OUT == OUT_SITU;
+  constexpr bool GATHER = gathers<OUT, CG>();
   int stage = 0;
   uint32_t phase = 0, issued = 0, issued_phase = 0;
   bool ok = true;
@@ -183,8 +187,9 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
 // Scale words of four K blocks of a tile: of 128 rows of A, four per lane (rows
 // lane + 32 j), and of the two weight blocks.
 struct ScaleRows {
-  int row[4];                // rows of A, -1: none (its product is not stored, or of zeros)
-  const uint32_t *w0, *w1;   // words of the two weight blocks
+  int row[4];   // rows of A, -1: none (its product is not stored, or of zeros)
+  int64_t at;   // first word of the weight block (SiTU: in both matrices)
+  int second;   // words from there to the second block's
 };
 struct ScaleWords {
   uint32_t a[4], b0, b1;
@@ -192,58 +197,48 @@ struct ScaleWords {
 template <int OUT, int CG>
 __device__ __forceinline__ ScaleRows scale_rows(const Params& p, const Tile& tl) {
   const int lane = threadIdx.x & 31;
-  ScaleRows r{{-1, -1, -1, -1}, nullptr, nullptr};
   const int nb0 = OUT == OUT_SITU ? tl.n : 2 * tl.n;
-  const int64_t at = ((int64_t)tl.e * p.w_blocks + nb0) * p.words;
-  r.w0 = p.w_words + at;
-  r.w1 = OUT == OUT_SITU ? p.w_up_words + at : nb0 + 1 < p.w_blocks ? r.w0 + p.words : r.w0;
+  ScaleRows r{{-1, -1, -1, -1}, ((int64_t)tl.e * p.w_blocks + nb0) * p.words,
+              nb0 + 1 < p.w_blocks ? p.words : 0};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int i = lane + 32 * j;
-    if (i < tl.rows) r.row[j] = OUT == OUT_SITU ? p.index[tl.m0 + i] : tl.m0 + i;
+    if (i < tl.rows) r.row[j] = gathers<OUT, CG>() ? p.index[tl.m0 + i] : tl.m0 + i;
     if (r.row[j] >= p.a_rows) r.row[j] = -1;
   }
   return r;
 }
+template <int OUT>
 __device__ __forceinline__ ScaleWords scale_words(const Params& p, const ScaleRows& r, int q) {
   ScaleWords w{{0, 0, 0, 0}, 0, 0};
+  const uint32_t* a = p.a_words + (int64_t)q * p.a_rows;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (r.row[j] >= 0) w.a[j] = p.a_words[(int64_t)q * p.a_rows + r.row[j]];
-  w.b0 = r.w0[q];
-  w.b1 = r.w1[q];
+    if (r.row[j] >= 0) w.a[j] = a[r.row[j]];
+  w.b0 = p.w_words[r.at + q];
+  w.b1 = OUT == OUT_SITU ? p.w_up_words[r.at + q] : p.w_words[r.at + r.second + q];
   return w;
 }
-
-// Rows of A by index (SiTU), 32 per warp: 16-byte asynchronous copies into the
-// swizzled layout a TMA load would leave.  Every copy reads inside its row, so
-// that none needs zero-filling (whose branches took longer): columns past n_in
-// repeat the last ones (they meet zeros of W), rows past the tile repeat its
-// last row (never stored), and an index outside A reads row 0 (its scale words
-// are 0, and so is its product).
-__device__ __forceinline__ void load_index(const Params& p, const Tile& tl, int row0, int (&row)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = min(row0 + 4 * i, tl.rows - 1);
-    row[i] = r >= 0 ? p.index[tl.m0 + r] : 0;
-    if ((uint32_t)row[i] >= (uint32_t)p.a_rows) row[i] = 0;
-  }
-}
-
 // The four row warps.  Scales: warp w writes the words to TMEM lanes 32 w ...:
 // columns 0-3 the words of rows 0-31, 32-63, 64-95 and 96-127 of A, 4-7 and
 // 8-11 those of the two weight blocks (one word for their 128 rows), the same in
 // each quarter, as the block-scaled MMA reads them.  Words, row numbers and
 // tiles are loaded one step ahead.
-// SiTU: a stage of A is announced once its copies have landed; up to IN_FLIGHT
-// stages stay in flight, but none while the ring is full, when the tensor cores
-// may be waiting for exactly these.
-constexpr int IN_FLIGHT = 2;
+// Rows of A by index (GATHER), 32 per warp: 16-byte asynchronous copies into the
+// swizzled layout a TMA load would leave.  (TMA's own gather of four rows took
+// about 100 cycles an instruction.)  Every copy reads inside its row, so that
+// none needs zero-filling: columns past n_in repeat the last ones (they meet
+// zeros of W), rows past the tile repeat its last row (never stored), and an
+// index outside A reads row 0 (its scale words are 0, and so is its product).
+// A stage of A is announced once its copies have landed; up to IN_FLIGHT stages
+// stay in flight, but none while the ring is full, when the tensor cores may be
+// waiting for exactly these.
+constexpr int IN_FLIGHT = 2, COPIES = 32 / ROW_WARPS;
 template <int OUT, int CG>
 __device__ void feed_rows(const Params& p, uint32_t ring, uint32_t tmem, Sync& s, Unit u) {
   using C = Cfg<CG>;
-  constexpr bool GATHER = OUT == OUT_SITU;
-  const int lane = threadIdx.x & 31, first = 32 * ((threadIdx.x >> 5) & 3);
+  constexpr bool GATHER = gathers<OUT, CG>();
+  const int lane = threadIdx.x & 31, first = threadIdx.x & 96;
   const int chunk = lane & 7, row0 = first + (lane >> 3);
   const int total = total_tiles<CG>(p);
   const uint32_t sfull0 = CG == 1 ? smem_u32(s.sfull) : map_to_rank(smem_u32(s.sfull), 0);
@@ -251,37 +246,39 @@ __device__ void feed_rows(const Params& p, uint32_t ring, uint32_t tmem, Sync& s
   int sstage = 0, stage = 0, head = 0;  // next scale stage, next stage, oldest stage in flight
   uint32_t sphase = 0, phase = 0;
   int flying = 0;
+  bool ok = true;
   auto announce = [&]() {  // the oldest stage in flight, once it has landed
     if (flying == 1) cp_async_wait<0>();
     else if (flying == 2) cp_async_wait<1>();
     else cp_async_wait<2>();
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(full0 + 8 * head);  // a pair's second CTA relays it to the leader
+    if (lane == 0) mbar_arrive(full0 + 8 * head);
     if (++head == C::STAGES) head = 0;
     --flying;
   };
   Tile tl = own_rows<CG>(tile_ahead<CG>(p, u.first, total), u.rank);
   Tile tn = own_rows<CG>(tile_ahead<CG>(p, u.first + u.step, total), u.rank);
-  int row[8];  // GATHER: of the next tile
-  if (GATHER) load_index(p, tl, row0, row);
   ScaleRows rows = scale_rows<OUT, CG>(p, tl);
-  ScaleWords next = scale_words(p, rows, 0);
-  bool ok = true;
+  ScaleWords next = scale_words<OUT>(p, rows, 0);
   for (int t = u.first; ok && t < total; t += u.step) {
-    const uint8_t* at[8];
+    uint32_t at[COPIES];  // rows of A, in 16-byte chunks
     if (GATHER) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) at[i] = p.a + (int64_t)row[i] * p.n_in;
-      load_index(p, tn, row0, row);
+      for (int i = 0; i < COPIES; ++i) {
+        const int r = min(row0 + 4 * i, tl.rows - 1);
+        uint32_t row = r >= 0 ? (uint32_t)p.index[tl.m0 + r] : 0u;
+        if (row >= (uint32_t)p.a_rows) row = 0;
+        at[i] = row * (uint32_t)(p.n_in >> 4);
+      }
     }
     const ScaleRows rows1 = scale_rows<OUT, CG>(p, tn);
-    const Tile after = own_rows<CG>(tile_ahead<CG>(p, t + 2 * u.step, total), u.rank);
     for (int kb = 0; kb < p.kb; kb += GATHER ? 1 : 4) {
       if (!GATHER || (kb & 3) == 0) {
         const ScaleWords w = next;
         const int q = (kb >> 2) + 1;
-        next = q < p.words ? scale_words(p, rows, q) : scale_words(p, rows1, 0);
+        if (q == p.words) rows = rows1;
+        next = scale_words<OUT>(p, rows, q < p.words ? q : 0);
         ok = warp_wait(smem_u32(&s.sempty[sstage]), sphase ^ 1u, &s.abort_flag, p.status);
         if (!ok) break;
         fence_after();
@@ -302,19 +299,19 @@ __device__ void feed_rows(const Params& p, uint32_t ring, uint32_t tmem, Sync& s
       if (GATHER) {
         const uint32_t empty = smem_u32(&s.empty[stage]);
         while (flying > 0 && (flying > IN_FLIGHT ||
-                              !__all_sync(0xffffffffu, mbar_try_wait(empty, phase ^ 1u))))
+                              !__all_sync(0xffffffffu, mbar_test(empty, phase ^ 1u))))
           announce();
         ok = warp_wait(empty, phase ^ 1u, &s.abort_flag, p.status);
         if (!ok) break;
         const uint32_t dst = ring + stage * C::STAGE_BYTES + row0 * BK;
-        const int col = min(kb * BK + chunk * 16, p.n_in - 16);
+        const uint32_t col = min(kb * (BK / 16) + chunk, (p.n_in >> 4) - 1);
         // row0 + 4 i: its last three bits alternate between two values
         const uint32_t dst0 = dst + ((chunk ^ (row0 & 7)) << 4);
         const uint32_t dst1 = dst + 4 * BK + ((chunk ^ ((row0 + 4) & 7)) << 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < COPIES; ++i)
           if (first + 4 * i < tl.rows)
-            cp_async16((i & 1 ? dst1 : dst0) + (i >> 1) * 8 * BK, at[i] + col);
+            cp_async16((i & 1 ? dst1 : dst0) + (i >> 1) * 8 * BK, p.a + (uint64_t)(at[i] + col) * 16);
         cp_async_commit();
         ++flying;
         if (++stage == C::STAGES) {
@@ -323,31 +320,11 @@ __device__ void feed_rows(const Params& p, uint32_t ring, uint32_t tmem, Sync& s
         }
       }
     }
-    rows = rows1;
     tl = tn;
-    tn = after;
+    tn = own_rows<CG>(tile_ahead<CG>(p, t + 2 * u.step, total), u.rank);
   }
   if (!ok) cp_async_wait<0>();
   while (ok && flying > 0) announce();
-}
-
-// The second CTA of a pair passes the landed stages of its rows on to the
-// leader's barriers.
-template <int CG>
-__device__ void relay_rows(const Params& p, Sync& s, Unit u) {
-  const int total = total_tiles<CG>(p);
-  const uint32_t lead0 = map_to_rank(smem_u32(s.full), 0);
-  int stage = 0;
-  uint32_t phase = 0;
-  for (int t = u.first; t < total; t += u.step)
-    for (int kb = 0; kb < p.kb; ++kb) {
-      if (!mbar_wait(smem_u32(&s.full[stage]), phase, &s.abort_flag, p.status)) return;
-      mbar_arrive_remote(lead0 + 8 * stage);
-      if (++stage == Cfg<CG>::STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
 }
 
 // The whole warp walks the tiles, so that addresses and descriptors stay in
@@ -642,10 +619,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                          : Unit{(int)(blockIdx.x >> 1), (int)(gridDim.x >> 1), (int)cluster_rank()};
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      // the producer's bytes, and SiTU the row warps (of a pair's second CTA
-      // through its own barriers, which only they use, and the relay)
-      mbar_init(smem_u32(&s.full[i]),
-                OUT != OUT_SITU ? 1 : u.rank == 1 ? ROW_WARPS : 1 + ROW_WARPS + (CG == 2 ? 1 : 0));
+      mbar_init(smem_u32(&s.full[i]), 1 + (gathers<OUT, CG>() ? ROW_WARPS : 0));
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < SF_STAGES; ++i) {
@@ -675,7 +649,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       if ((threadIdx.x & 31) == 0) produce<OUT, CG>(p, ring, s, u);
     } else if (warp == 1) {
       if (u.rank == 0) issue_mmas<OUT, CG>(p, ring, tmem, s, u);
-      else if (OUT == OUT_SITU && (threadIdx.x & 31) == 0) relay_rows<CG>(p, s, u);
     }
   } else if (warp < ROW_WARP0) {
     regs_inc<REGS_EPI>();
@@ -773,8 +746,9 @@ cudaError_t launch(const Params& p, bool pairs, int64_t max_tiles, cudaStream_t 
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st) {
   if (g.rows == 0) return cudaSuccess;
   Params p{};
-  if (g.situ != (g.index != nullptr)) return cudaErrorInvalidValue;
-  bool ok = (g.situ || (make_map(&p.tmA, g.a, g.n_in, g.a_rows, 1, BM, 2) &&
+  const bool gather = g.situ && !g.pairs;
+  if (gather != (g.index != nullptr)) return cudaErrorInvalidValue;
+  bool ok = (gather || (make_map(&p.tmA, g.a, g.n_in, g.a_rows, 1, BM, 2) &&
                         make_map(&p.tmA32, g.a, g.n_in, g.a_rows, 1, SMALL_ROWS, 2))) &&
             make_map(&p.tmB0, g.w, g.n_in, g.n_out, g.R, SUB, 3) &&
             (!g.situ || make_map(&p.tmB1, g.w_up, g.n_in, g.n_out, g.R, SUB, 3));

@@ -45,7 +45,8 @@ struct Fp8Gemm {
   const uint8_t* a_scales;  // [words, a_rows, 4]
   int64_t a_rows;
   // with index, row r of the product is a[index[r]] (zeros outside [0, a_rows));
-  // without, a[r] and a_rows = rows.  SiTU only.
+  // without, a[r] and a_rows = rows.  SiTU on single CTAs needs it, the others
+  // do not take it.
   const int32_t* index;
   int64_t rows;
   int R, n_in, n_out;
