@@ -437,54 +437,89 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Two fp32 values in one register pair, for the packed instructions: half the
+// issue slots of the polynomials below.
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 both(float a) { return pack2(a, a); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // tanh(x) / x as polynomials in u = x^2, fitted by least squares with the
 // weights moved towards the largest relative error: relative error in 32 bits
 // at most 4.2 * 2^-24 for |x| <= kGateX, 1.9 * 2^-24 for |x| <= kUpX.
 constexpr float kGateX = 1.5f, kUpX = 0.5f;
-__device__ __forceinline__ float gate_poly(float u) {
-  float p = 2.553440027e-05f;
-  p = fmaf(p, u, -3.205151297e-04f);
-  p = fmaf(p, u, 1.872322173e-03f);
-  p = fmaf(p, u, -7.067439146e-03f);
-  p = fmaf(p, u, 2.066442743e-02f);
-  p = fmaf(p, u, -5.348970741e-02f);
-  p = fmaf(p, u, 1.332349330e-01f);
-  p = fmaf(p, u, -3.333253562e-01f);
-  return fmaf(p, u, 9.999998808e-01f);
+__device__ __forceinline__ f32x2 gate_poly(f32x2 u) {
+  f32x2 p = both(2.553440027e-05f);
+  p = fma2(p, u, both(-3.205151297e-04f));
+  p = fma2(p, u, both(1.872322173e-03f));
+  p = fma2(p, u, both(-7.067439146e-03f));
+  p = fma2(p, u, both(2.066442743e-02f));
+  p = fma2(p, u, both(-5.348970741e-02f));
+  p = fma2(p, u, both(1.332349330e-01f));
+  p = fma2(p, u, both(-3.333253562e-01f));
+  return fma2(p, u, both(9.999998808e-01f));
 }
-__device__ __forceinline__ float up_poly(float u) {
-  float p = 1.713500172e-02f;
-  p = fmaf(p, u, -5.298607424e-02f);
-  p = fmaf(p, u, 1.332477927e-01f);
-  p = fmaf(p, u, -3.333306909e-01f);
-  return fmaf(p, u, 1.0f);
+__device__ __forceinline__ f32x2 up_poly(f32x2 u) {
+  f32x2 p = both(1.713500172e-02f);
+  p = fma2(p, u, both(-5.298607424e-02f));
+  p = fma2(p, u, both(1.332477927e-01f));
+  p = fma2(p, u, both(-3.333306909e-01f));
+  return fma2(p, u, both(1.0f));
 }
-// SiTU-GLU hidden unit beta1 tanh(a / beta1) sigmoid(a) beta2 tanh(c / beta2)
-// to a few 2^-24 of its value: the hidden unit is rounded to e4m3 next, and a
-// coarser value would fall on the other side of a rounding border more often.
-// Near zero, tanh(x) = x P(x^2): no cancellation, and beta tanh(a / beta) =
-// a P.  Beyond (WIDE; |x| > kGateX, kUpX), tanh(x) = (1 - t) / (1 + t) with
-// t = e^(-2 |x|), its denominator shared with the sigmoid's.
+// Two SiTU-GLU hidden units beta1 tanh(a / beta1) sigmoid(a) beta2 tanh(c / beta2),
+// in place of a, to a few 2^-24 of their value: a hidden unit is rounded to e4m3
+// next, and a coarser value would fall on the other side of a rounding border
+// more often.  Near zero, tanh(x) = x P(x^2): no cancellation, and
+// beta tanh(a / beta) = a P.  Beyond (WIDE; |x| > kGateX, kUpX), tanh(x) =
+// (1 - t) / (1 + t) with t = e^(-2 |x|), its denominator shared with the
+// sigmoid's.
+constexpr float kLog2e = 1.4426950408889634f;
 template <bool WIDE>
-__device__ __forceinline__ float situ_unit(float a, float c, float b1, float b2, float i1, float i2) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  const float x1 = a * i1, x2 = c * i2;
-  float n1 = a * gate_poly(x1 * x1), n2 = c * up_poly(x2 * x2);
-  float d = 1.0f + ex2(-kLog2e * a);
+__device__ __forceinline__ void situ_units(float& a0, float& a1, float c0, float c1, float b1,
+                                           float b2, float i1, float i2) {
+  const f32x2 a = pack2(a0, a1), c = pack2(c0, c1);
+  const f32x2 x1 = mul2(a, both(i1)), x2 = mul2(c, both(i2));
+  f32x2 n1 = mul2(a, gate_poly(mul2(x1, x1))), n2 = mul2(c, up_poly(mul2(x2, x2)));
+  float d0 = 1.0f + ex2(-kLog2e * a0), d1 = 1.0f + ex2(-kLog2e * a1);
   if (WIDE) {
-    const float t1 = ex2(-2.0f * kLog2e * fabsf(x1)), t2 = ex2(-2.0f * kLog2e * fabsf(x2));
-    float e1 = 1.0f, e2 = 1.0f;
-    if (fabsf(x1) > kGateX) {
-      n1 = copysignf(b1 - b1 * t1, a);
-      e1 = 1.0f + t1;
+    float n[2][2], d[2] = {d0, d1};
+    unpack2(n1, n[0][0], n[0][1]);
+    unpack2(n2, n[1][0], n[1][1]);
+    const float av[2] = {a0, a1}, cv[2] = {c0, c1};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float xa = fabsf(av[i] * i1), xc = fabsf(cv[i] * i2);
+      const float t1 = ex2(-2.0f * kLog2e * xa), t2 = ex2(-2.0f * kLog2e * xc);
+      if (xa > kGateX) {
+        n[0][i] = copysignf(b1 - b1 * t1, av[i]);
+        d[i] *= 1.0f + t1;
+      }
+      if (xc > kUpX) {
+        n[1][i] = copysignf(b2 - b2 * t2, cv[i]);
+        d[i] *= 1.0f + t2;
+      }
     }
-    if (fabsf(x2) > kUpX) {
-      n2 = copysignf(b2 - b2 * t2, c);
-      e2 = 1.0f + t2;
-    }
-    d *= e1 * e2;
+    n1 = pack2(n[0][0], n[0][1]);
+    n2 = pack2(n[1][0], n[1][1]);
+    d0 = d[0];
+    d1 = d[1];
   }
-  return n1 * n2 * rcp(d);
+  unpack2(mul2(mul2(n1, n2), pack2(rcp(d0), rcp(d1))), a0, a1);
 }
 
 // A tile's hidden units of this warp: 32 rows x 32 units, quantised with the
@@ -505,12 +540,12 @@ __device__ __forceinline__ void finish_situ(const Params& p, const Tile& tl, flo
     const float i1 = 1.0f / p.beta1, i2 = 1.0f / p.beta2;
     if (__any_sync(0xffffffffu, ma * i1 > kGateX || mc * i2 > kUpX)) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        v[i] = situ_unit<true>(v[i], v[32 + i], p.beta1, p.beta2, i1, i2);
+      for (int i = 0; i < 32; i += 2)
+        situ_units<true>(v[i], v[i + 1], v[32 + i], v[33 + i], p.beta1, p.beta2, i1, i2);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        v[i] = situ_unit<false>(v[i], v[32 + i], p.beta1, p.beta2, i1, i2);
+      for (int i = 0; i < 32; i += 2)
+        situ_units<false>(v[i], v[i + 1], v[32 + i], v[33 + i], p.beta1, p.beta2, i1, i2);
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));  // finite, or NaN: left out

@@ -42,26 +42,45 @@ __device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& v, float (&f)
     f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-template <typename T>
+// Largest magnitude of a vector, NaN left out; FINITE leaves infinities out too
+// (the kernels take that way only for a block whose first answer is infinite).
+template <typename T, bool FINITE>
 __device__ __forceinline__ float vec_amax(const uint4& v) {
-  float f[kVec<T>];
-  unpack<T>(v, f);
-  float m = 0.0f;
+  if constexpr (kVec<T> == 8 && !FINITE) {  // bf16 pairs: 8 instructions
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])),
+                                     __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.0f);  // 0 where all are NaN
+  } else {
+    float f[kVec<T>];
+    unpack<T>(v, f);
+    float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kVec<T>; ++i) m = finite_max(m, f[i]);
-  return m;
+    for (int i = 0; i < kVec<T>; ++i) m = FINITE ? finite_max(m, f[i]) : fmaxf(m, fabsf(f[i]));
+    return m;
+  }
 }
 // Quantises the vector's elements and stores them at q (4 or 8 bytes).
-template <typename T>
+template <typename T, bool FINITE>
 __device__ __forceinline__ void store_q(uint8_t* q, const uint4& v, float inv) {
   float f[kVec<T>];
   unpack<T>(v, f);
   uint32_t w[kVec<T> / 4];
 #pragma unroll
-  for (int i = 0; i < kVec<T> / 4; ++i)
-    w[i] = pack_e4m3(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv, f[4 * i + 3] * inv);
+  for (int i = 0; i < kVec<T> / 4; ++i) {
+    const float a = f[4 * i] * inv, b = f[4 * i + 1] * inv, c = f[4 * i + 2] * inv,
+                d = f[4 * i + 3] * inv;
+    w[i] = FINITE ? pack_e4m3(a, b, c, d) : pack_e4m3_finite(a, b, c, d);
+  }
   if constexpr (kVec<T> == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
   else *reinterpret_cast<uint32_t*>(q) = w[0];
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float m) {
+#pragma unroll
+  for (int off = LANES / 2; off > 0; off >>= 1)
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return m;
 }
 
 // One warp per row.  A block's 128 elements lie in kBlockLanes lanes (16 for
@@ -100,12 +119,15 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = v0 + u * 32 + lane;
-      float m = vec_amax<T>(v[u]);
-#pragma unroll
-      for (int off = BL / 2; off > 0; off >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      uint8_t* dst = q + r * cols + (int64_t)at * V;
+      float m = lanes_max<BL>(vec_amax<T, false>(v[u]));
+      if (__any_sync(0xffffffffu, m == INFINITY)) {
+        m = lanes_max<BL>(vec_amax<T, true>(v[u]));
+        if (at < nvec) store_q<T, true>(dst, v[u], pow2_f(-scale_exponent(m)));
+      } else if (at < nvec) {
+        store_q<T, false>(dst, v[u], pow2_f(-scale_exponent(m)));
+      }
       const int e = scale_exponent(m);
-      if (at < nvec) store_q<T>(q + r * cols + (int64_t)at * V, v[u], pow2_f(-e));
       const int b = at / BL;
       if (lane % BL == 0 && b < blocks4)
         scales[((int64_t)(b >> 2) * rows + r) * 4 + (b & 3)] = (uint8_t)(e + 127);
@@ -130,7 +152,6 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const T* __restri
   const int c = cbi * kQBlock + (threadIdx.x % BL) * V;
   const int64_t r0 = (int64_t)rbi * kQBlock + threadIdx.x / BL;
   uint4 v[U];
-  float m = 0.0f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     v[u] = make_uint4(0, 0, 0, 0);
@@ -138,20 +159,33 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const T* __restri
     if (c < cols && r < rows)
       v[u] = *reinterpret_cast<const uint4*>(w + (mat * rows + r) * cols + c);
   }
+  float m = 0.0f;
 #pragma unroll
-  for (int u = 0; u < U; ++u) m = fmaxf(m, vec_amax<T>(v[u]));
+  for (int u = 0; u < U; ++u) m = fmaxf(m, vec_amax<T, false>(v[u]));
+  bool finite = true;  // of the block's maximum
+  for (int pass = 0; pass < 2; ++pass) {
+    m = lanes_max<32>(m);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-  __syncthreads();
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
+    if (m < INFINITY) break;
+    finite = false;
+    m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
+    for (int u = 0; u < U; ++u) m = fmaxf(m, vec_amax<T, true>(v[u]));
+    __syncthreads();
+  }
   const int e = scale_exponent(m);
   const float inv = pow2_f(-e);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t r = r0 + u * RP;
-    if (c < cols && r < rows) store_q<T>(q + (mat * rows + r) * cols + c, v[u], inv);
+    if (c < cols && r < rows) {
+      uint8_t* dst = q + (mat * rows + r) * cols + c;
+      if (finite) store_q<T, false>(dst, v[u], inv);
+      else store_q<T, true>(dst, v[u], inv);
+    }
   }
   if (threadIdx.x == 0) scales[blk] = (uint8_t)(e + 127);
 }
