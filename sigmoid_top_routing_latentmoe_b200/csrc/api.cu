@@ -336,13 +336,13 @@ static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* of
   return t;
 }
 
-// The rows of z quantised, gate and up products with the SiTU and the
-// quantisation of the hidden units in their epilogue, output product.  On CTA
-// pairs the rows are quantised in sorted order; on single CTAs once per token,
-// and the products gather each pair's row (K3-width prompt batch: a sorted copy
-// is 470 MB to write and to read).  The quantised rows take the first half of
-// the workspace's sorted-row area (rows of 2 or 4 bytes an element) and their
-// scales the second; the hidden units likewise theirs.
+// The rows of z quantised once per token, gate and up products with the SiTU
+// and the quantisation of the hidden units in their epilogue, output product.
+// On CTA pairs the quantised rows are copied into sorted order first; on single
+// CTAs the products gather each pair's row.  Areas of the workspace (2 or 4
+// bytes for each of their elements): the rows the products read, then their
+// scales, take the sorted-row area; the hidden units and theirs the hidden-unit
+// area; the rows before sorting the expert-output area.
 template <typename T>
 static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const int32_t* perm,
                                       const int32_t* offsets, const lmoe_fp8_experts* w, void* out,
@@ -361,9 +361,13 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   {
     ProfScope ps("quantize", st);
     LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");
-    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, pairs ? perm : nullptr,
-                                      pairs ? P : d->n_tokens, Lt, zq, zs, st),
+    uint8_t* tq = pairs ? at<uint8_t>(ws, L.eo) : zq;
+    uint8_t* ts = pairs ? tq + d->n_tokens * Lt : zs;
+    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, nullptr, d->n_tokens, Lt, tq,
+                                      ts, st),
               "quantize rows");
+    if (pairs)
+      LMOE_CUDA(launch_sort_rows(tq, ts, d->n_tokens, perm, P, Lt, zq, zs, st), "sort rows");
   }
   Fp8Gemm g{};
   g.rows = P; g.R = d->n_routed; g.tiles = tl.tiles; g.n_mtiles = tl.n_mtiles;

@@ -33,6 +33,10 @@ template <typename T>
 cudaError_t launch_quantize_rows(const T* x, int64_t n_src, int64_t ld, const int32_t* index,
                                  int64_t rows, int cols, uint8_t* q, uint8_t* scales,
                                  cudaStream_t st);
+// Quantised rows in another order: row r is row index[r], zeros outside [0, n_src).
+cudaError_t launch_sort_rows(const uint8_t* q, const uint8_t* scales, int64_t n_src,
+                             const int32_t* index, int64_t rows, int cols, uint8_t* q_out,
+                             uint8_t* scales_out, cudaStream_t st);
 // q [mats, rows, cols] e4m3 and scales [mats, ceil(rows / 128), 4 words] of w.
 template <typename T>
 cudaError_t launch_quantize_weights(const T* w, int64_t mats, int64_t rows, int cols, uint8_t* q,

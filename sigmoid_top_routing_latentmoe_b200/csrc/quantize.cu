@@ -60,18 +60,22 @@ __device__ __forceinline__ float vec_amax(const uint4& v) {
     return m;
   }
 }
-// Quantises the vector's elements and stores them at q (4 or 8 bytes).
+// Quantises the vector's elements, four to a word.
 template <typename T, bool FINITE>
-__device__ __forceinline__ void store_q(uint8_t* q, const uint4& v, float inv) {
+__device__ __forceinline__ void quantize_vec(const uint4& v, float inv, uint32_t* w) {
   float f[kVec<T>];
   unpack<T>(v, f);
-  uint32_t w[kVec<T> / 4];
 #pragma unroll
   for (int i = 0; i < kVec<T> / 4; ++i) {
     const float a = f[4 * i] * inv, b = f[4 * i + 1] * inv, c = f[4 * i + 2] * inv,
                 d = f[4 * i + 3] * inv;
     w[i] = FINITE ? pack_e4m3(a, b, c, d) : pack_e4m3_finite(a, b, c, d);
   }
+}
+template <typename T, bool FINITE>
+__device__ __forceinline__ void store_q(uint8_t* q, const uint4& v, float inv) {
+  uint32_t w[kVec<T> / 4];
+  quantize_vec<T, FINITE>(v, inv, w);
   if constexpr (kVec<T> == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
   else *reinterpret_cast<uint32_t*>(q) = w[0];
 }
@@ -83,21 +87,57 @@ __device__ __forceinline__ float lanes_max(float m) {
   return m;
 }
 
-// One warp per row.  A block's 128 elements lie in kBlockLanes lanes (16 for
-// bf16, 32 for fp32), so one warp-wide load covers 2 or 1 blocks; U loads are
-// in flight before the first maximum.
+// One warp per row, 512 columns a step: a lane holds 16 neighbouring elements,
+// eight lanes a block, and the step's four exponents are one word of scales.
+// The kernel is bound by issue slots rather than bytes (with 8 elements a lane,
+// 140 instructions for every 8, the mid layer's 131072 rows of 1024 took 72 us),
+// so 16 elements share the reductions and addresses.
+constexpr int kLaneElems = 16, kStepCols = 32 * kLaneElems, kRowWarps = 8;
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ x, int64_t n_src,
-                                                            int64_t ld,
-                                                            const int32_t* __restrict__ index,
-                                                            int64_t rows, int cols,
-                                                            uint8_t* __restrict__ q,
-                                                            uint8_t* __restrict__ scales) {
+struct LaneElems {
+  uint4 v[kLaneElems / kVec<T>];
+};
+template <typename T>
+__device__ __forceinline__ LaneElems<T> load_elems(const T* x, bool have) {
+  LaneElems<T> e;
+#pragma unroll
+  for (int i = 0; i < kLaneElems / kVec<T>; ++i)
+    e.v[i] = have ? reinterpret_cast<const uint4*>(x)[i] : make_uint4(0, 0, 0, 0);
+  return e;
+}
+template <typename T, bool FINITE>
+__device__ __forceinline__ float lane_amax(const LaneElems<T>& e) {
+  if constexpr (kVec<T> == 8 && !FINITE) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(e.v);
+    __nv_bfloat162 m = __habs2(h[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(h[i]));
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.0f);
+  } else {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLaneElems / kVec<T>; ++i) m = fmaxf(m, vec_amax<T, FINITE>(e.v[i]));
+    return m;
+  }
+}
+template <typename T, bool FINITE>
+__device__ __forceinline__ uint4 lane_q(const LaneElems<T>& e, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < kLaneElems / kVec<T>; ++i)
+    quantize_vec<T, FINITE>(e.v[i], inv, w + i * kVec<T> / 4);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowWarps)
+    quantize_rows_kernel(const T* __restrict__ x, int64_t n_src, int64_t ld,
+                         const int32_t* __restrict__ index, int64_t rows, int cols,
+                         uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   pdl_trigger();
   pdl_wait();
-  constexpr int V = kVec<T>, BL = kQBlock / V, U = 4;
+  constexpr int U = 2;  // steps whose loads are in flight together
   const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t r = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   if (r >= rows) return;
   int64_t src = r;
   bool have = true;
@@ -105,32 +145,32 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
     src = index[r];
     have = src >= 0 && src < n_src;
   }
-  const uint4* xr = reinterpret_cast<const uint4*>(x + (have ? src : 0) * ld);
-  const int nvec = cols / V;
-  const int blocks = (cols + kQBlock - 1) / kQBlock, blocks4 = (blocks + 3) & ~3;
-  for (int v0 = 0; v0 * V < blocks4 * kQBlock; v0 += 32 * U) {
-    uint4 v[U];
+  const int steps = (cols + kStepCols - 1) / kStepCols;
+  const T* xr = x + (have ? src : 0) * ld + lane * kLaneElems;
+  uint8_t* qr = q + r * cols + lane * kLaneElems;
+  uint8_t* sr = scales + r * 4 + (lane >> 3);
+  // a long row of few rows is shared by gridDim.y warps
+  for (int s0 = blockIdx.y * U; s0 < steps; s0 += gridDim.y * U) {
+    LaneElems<T> e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      e[u] = load_elems(xr + (s0 + u) * kStepCols,
+                        have && (s0 + u) * kStepCols + lane * kLaneElems < cols);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = v0 + u * 32 + lane;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (have && at < nvec) v[u] = xr[at];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = v0 + u * 32 + lane;
-      uint8_t* dst = q + r * cols + (int64_t)at * V;
-      float m = lanes_max<BL>(vec_amax<T, false>(v[u]));
+      const int step = s0 + u;
+      if (step >= steps) break;
+      const bool in = step * kStepCols + lane * kLaneElems < cols;
+      float m = lanes_max<8>(lane_amax<T, false>(e[u]));
+      uint4 w;
       if (__any_sync(0xffffffffu, m == INFINITY)) {
-        m = lanes_max<BL>(vec_amax<T, true>(v[u]));
-        if (at < nvec) store_q<T, true>(dst, v[u], pow2_f(-scale_exponent(m)));
-      } else if (at < nvec) {
-        store_q<T, false>(dst, v[u], pow2_f(-scale_exponent(m)));
+        m = lanes_max<8>(lane_amax<T, true>(e[u]));
+        w = lane_q<T, true>(e[u], pow2_f(-scale_exponent(m)));
+      } else {
+        w = lane_q<T, false>(e[u], pow2_f(-scale_exponent(m)));
       }
-      const int e = scale_exponent(m);
-      const int b = at / BL;
-      if (lane % BL == 0 && b < blocks4)
-        scales[((int64_t)(b >> 2) * rows + r) * 4 + (b & 3)] = (uint8_t)(e + 127);
+      if (in) *reinterpret_cast<uint4*>(qr + step * kStepCols) = w;
+      if ((lane & 7) == 0) sr[(int64_t)step * rows * 4] = (uint8_t)(scale_exponent(m) + 127);
     }
   }
 }
@@ -190,6 +230,35 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const T* __restri
   if (threadIdx.x == 0) scales[blk] = (uint8_t)(e + 127);
 }
 
+// Rows of q and their scale words in sorted order, one warp per row.
+__global__ void __launch_bounds__(32 * kRowWarps)
+    sort_rows_kernel(const uint8_t* __restrict__ q, const uint32_t* __restrict__ words, int64_t n_src,
+                     const int32_t* __restrict__ index, int64_t rows, int cols, int n_words,
+                     uint8_t* __restrict__ q_out, uint32_t* __restrict__ words_out) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int U = 4;  // loads in flight
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const int64_t src = index[r];
+  const bool have = src >= 0 && src < n_src;
+  const int nvec = cols / 16;
+  const uint4* from = reinterpret_cast<const uint4*>(q + (have ? src : 0) * cols);
+  uint4* to = reinterpret_cast<uint4*>(q_out + r * cols);
+  for (int w = lane; w < n_words; w += 32)  // 0x7f: scale 1
+    words_out[w * rows + r] = have ? words[w * n_src + src] : 0x7f7f7f7fu;
+  for (int v0 = lane; v0 < nvec; v0 += 32 * U) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = have && v0 + 32 * u < nvec ? from[v0 + 32 * u] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v0 + 32 * u < nvec) to[v0 + 32 * u] = v[u];
+  }
+}
+
 // The tile list of a ragged product: expert e's rows [offsets[e], offsets[e + 1])
 // in tiles of at most tile_m.  Offsets are clamped to an ascending order inside
 // [0, rows] and the list to max_tiles, so that no list leads a product out of
@@ -239,16 +308,30 @@ cudaError_t launch_quantize_rows(const T* x, int64_t n_src, int64_t ld, const in
                                  int64_t rows, int cols, uint8_t* q, uint8_t* scales,
                                  cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  const int warps = 8;
+  const unsigned blocks = (unsigned)((rows + kRowWarps - 1) / kRowWarps);
+  // few rows: their steps are spread over up to 8 warps each, towards 1200 blocks
+  const int pairs = (cols + 2 * kStepCols - 1) / (2 * kStepCols);
+  const unsigned split = std::min<unsigned>(std::min(pairs, 8), std::max(1u, 1200 / blocks));
   count_launch();
-  return launch_pdl(quantize_rows_kernel<T>, dim3((unsigned)((rows + warps - 1) / warps)),
-                    dim3(warps * 32), 0, st, 1, x, n_src, ld, index, rows, cols, q, scales);
+  return launch_pdl(quantize_rows_kernel<T>, dim3(blocks, split), dim3(32 * kRowWarps), 0, st, 1, x,
+                    n_src, ld, index, rows, cols, q, scales);
 }
 template cudaError_t launch_quantize_rows<float>(const float*, int64_t, int64_t, const int32_t*,
                                                  int64_t, int, uint8_t*, uint8_t*, cudaStream_t);
 template cudaError_t launch_quantize_rows<__nv_bfloat16>(const __nv_bfloat16*, int64_t, int64_t,
                                                          const int32_t*, int64_t, int, uint8_t*,
                                                          uint8_t*, cudaStream_t);
+
+cudaError_t launch_sort_rows(const uint8_t* q, const uint8_t* scales, int64_t n_src,
+                             const int32_t* index, int64_t rows, int cols, uint8_t* q_out,
+                             uint8_t* scales_out, cudaStream_t st) {
+  if (rows == 0) return cudaSuccess;
+  count_launch();
+  return launch_pdl(sort_rows_kernel, dim3((unsigned)((rows + kRowWarps - 1) / kRowWarps)),
+                    dim3(32 * kRowWarps), 0, st, 1, q, reinterpret_cast<const uint32_t*>(scales),
+                    n_src, index, rows, cols, q_words(cols), q_out,
+                    reinterpret_cast<uint32_t*>(scales_out));
+}
 
 template <typename T>
 cudaError_t launch_quantize_weights(const T* w, int64_t mats, int64_t rows, int cols, uint8_t* q,
