@@ -318,12 +318,14 @@ static lmoe_status run_route_grouped(const lmoe_dims* d, const RouteRule& rule, 
 }
 
 // ------------------------------------------------------- 8-bit routed experts
+// Tiles of the 8-bit products: CTA pairs over 256 rows once experts have 64 rows
+// on average, else single CTAs over 128 (LMOE_FP8_PAIRS=0 or 1 overrides it).
 static bool fp8_pairs(const lmoe_dims* d) {
   if (const char* v = getenv("LMOE_FP8_PAIRS")) {
     if (v[0] == '0') return false;
     if (v[0] == '1') return true;
   }
-  return d->n_tokens * (int64_t)d->top_k >= 256 * (int64_t)d->n_routed;
+  return d->n_tokens * (int64_t)d->top_k >= 64 * (int64_t)d->n_routed;
 }
 
 static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* offsets, void* ws) {
@@ -336,13 +338,18 @@ static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* of
   return t;
 }
 
-// The rows of z quantised once per token, gate and up products with the SiTU
-// and the quantisation of the hidden units in their epilogue, output product.
-// On CTA pairs the quantised rows are copied into sorted order first; on single
-// CTAs the products gather each pair's row.  Areas of the workspace (2 or 4
-// bytes for each of their elements): the rows the products read, then their
-// scales, take the sorted-row area; the hidden units and theirs the hidden-unit
-// area; the rows before sorting the expert-output area.
+// The rows of z in sorted order: with little to quantise in one kernel through
+// perm, else quantised once per token and then sorted in 8 bits (131072 rows of
+// 3584: 287 us in one kernel, 139 us in two).
+static bool fp8_sorts(const lmoe_dims* d) {
+  return d->top_k > 1 && d->n_tokens * (int64_t)d->top_k * d->latent >= (int64_t)1 << 24;
+}
+
+// Rows of z quantised in sorted order, gate and up products with the SiTU and
+// the quantisation of the hidden units in their epilogue, output product.
+// Areas of the workspace (2 or 4 bytes for each of their elements): the sorted
+// rows, then their scales, take the sorted-row area; the hidden units and theirs
+// the hidden-unit area; the rows before sorting the expert-output area.
 template <typename T>
 static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const int32_t* perm,
                                       const int32_t* offsets, const lmoe_fp8_experts* w, void* out,
@@ -361,12 +368,13 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   {
     ProfScope ps("quantize", st);
     LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");
-    uint8_t* tq = pairs ? at<uint8_t>(ws, L.eo) : zq;
-    uint8_t* ts = pairs ? tq + d->n_tokens * Lt : zs;
-    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, nullptr, d->n_tokens, Lt, tq,
-                                      ts, st),
+    const bool sorts = fp8_sorts(d);
+    uint8_t* tq = sorts ? at<uint8_t>(ws, L.eo) : zq;
+    uint8_t* ts = sorts ? tq + d->n_tokens * Lt : zs;
+    LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, sorts ? nullptr : perm,
+                                      sorts ? d->n_tokens : P, Lt, tq, ts, st),
               "quantize rows");
-    if (pairs)
+    if (sorts)
       LMOE_CUDA(launch_sort_rows(tq, ts, d->n_tokens, perm, P, Lt, zq, zs, st), "sort rows");
   }
   Fp8Gemm g{};
@@ -374,8 +382,7 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   g.pairs = pairs; g.max_tiles = tl.max_tiles; g.beta1 = d->beta1; g.beta2 = d->beta2;
   {
     ProfScope ps("expert_gemm1", st);
-    g.a = zq; g.a_scales = zs; g.a_rows = pairs ? P : d->n_tokens;
-    g.index = pairs ? nullptr : perm; g.n_in = Lt; g.n_out = F; g.situ = 1;
+    g.a = zq; g.a_scales = zs; g.n_in = Lt; g.n_out = F; g.situ = 1;
     g.w = (const uint8_t*)w->w_g; g.w_scales = w->w_g_scales;
     g.w_up = (const uint8_t*)w->w_u; g.w_up_scales = w->w_u_scales;
     g.out = hq; g.out_scales = hs;
@@ -383,7 +390,7 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   }
   {
     ProfScope ps("expert_gemm2", st);
-    g.a = hq; g.a_scales = hs; g.a_rows = P; g.index = nullptr; g.n_in = F; g.n_out = Lt; g.situ = 0;
+    g.a = hq; g.a_scales = hs; g.n_in = F; g.n_out = Lt; g.situ = 0;
     g.w = (const uint8_t*)w->w_o; g.w_scales = w->w_o_scales;
     g.out = out; g.out_f32 = std::is_same<T, float>::value ? 1 : 0;
     LMOE_CUDA(launch_fp8_gemm(g, status, st), "routed gemm2 (8-bit)");
@@ -1108,7 +1115,7 @@ lmoe_status moe_expert_gemm_fp8(const lmoe_dims* dims, int32_t n_in, int32_t n_o
   const Layout L = layout(dims, false);
   const TileList tl = tile_list(dims, L, offsets, ws);
   Fp8Gemm g{};
-  g.a = (const uint8_t*)a; g.a_scales = a_scales; g.a_rows = g.rows = tl.rows; g.R = dims->n_routed;
+  g.a = (const uint8_t*)a; g.a_scales = a_scales; g.rows = tl.rows; g.R = dims->n_routed;
   g.n_in = n_in; g.n_out = n_out; g.w = (const uint8_t*)w; g.w_scales = w_scales; g.out = out;
   g.out_f32 = dims->dtype == LMOE_F32 ? 1 : 0;
   g.pairs = tl.tile_m == kRoutedPairTileM;

@@ -11,8 +11,7 @@
 //   warp 0      TMA producer: A rows and two 128-row B boxes per K block,
 //   warp 1      MMA issuer and TMEM allocator,
 //   warps 4-19  epilogue, four per 32-row quarter, sharing its columns,
-//   warps 20-23 the scale words of four K blocks at a time, written to TMEM;
-//               SiTU on single CTAs: also the rows of A that p.index names.
+//   warps 20-23 the scale words of four K blocks at a time, written to TMEM.
 #include <cuda.h>
 
 #include <algorithm>
@@ -37,8 +36,8 @@ constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
 constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
 constexpr int TMEM_COLS = 512, SF_COL0 = 256;
 static_assert(SF_COL0 + SF_STAGES * SF_COLS <= TMEM_COLS, "TMEM");
-constexpr int EPI_WARP0 = 4, EPI_WARPS = 16, ROW_WARP0 = EPI_WARP0 + EPI_WARPS, ROW_WARPS = 4;
-constexpr int THREADS = 32 * (ROW_WARP0 + ROW_WARPS);
+constexpr int EPI_WARP0 = 4, EPI_WARPS = 16, SCALE_WARP0 = EPI_WARP0 + EPI_WARPS, SCALE_WARPS = 4;
+constexpr int THREADS = 32 * (SCALE_WARP0 + SCALE_WARPS);
 // Staging bytes of an epilogue warp.  SiTU stages 32 rows x 32 bytes, in the
 // first half; the second holds the rows' maxima (tile parity, warp of the
 // quarter, quarter and row).
@@ -65,12 +64,9 @@ struct Cfg {
 
 struct Params {
   CUtensorMap tmA, tmA32, tmB0, tmB1;
-  const uint8_t* a;                      // with index
-  const uint32_t* a_words;               // [words, a_rows]
-  const int32_t* index;
-  int a_rows;
+  const uint32_t* a_words;               // [words, rows]
   const uint32_t *w_words, *w_up_words;  // [R, w_blocks, words]
-  int rows, words, w_blocks, kb, n_tiles, n_in, n_out;
+  int rows, words, w_blocks, kb, n_tiles, n_out;
   const int4* tiles;
   const int32_t* n_mtiles;
   void* out;
@@ -78,10 +74,6 @@ struct Params {
   int32_t* status;
   float beta1, beta2;
 };
-
-// The gate and up products on single CTAs take their rows of A through p.index.
-template <int OUT, int CG>
-constexpr bool gathers() { return OUT == OUT_SITU && CG == 1; }
 
 // This CTA (or its pair): which of the tiles it takes, and its rank in the pair.
 struct Unit {
@@ -129,11 +121,9 @@ struct Sync {
 static_assert(Cfg<1>::SMEM_BYTES + sizeof(Sync) <= 232448 &&
                   Cfg<2>::SMEM_BYTES + sizeof(Sync) <= 232448, "shared memory");
 
-// Neighbouring rows of A come by TMA, those named by p.index from the row warps.
 template <int OUT, int CG>
 __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
   using C = Cfg<CG>;
-  constexpr bool GATHER = gathers<OUT, CG>();
   int stage = 0;
   uint32_t phase = 0, issued = 0, issued_phase = 0;
   bool ok = true;
@@ -146,8 +136,8 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
     const bool small = CG == 1 && tl.rows <= SMALL_ROWS, two = two_subs<OUT, CG>(p, tl);
     const CUtensorMap* map_a = small ? &p.tmA32 : &p.tmA;
     // a pair's second CTA loads no A when it has no rows (its accumulator is not stored)
-    const bool load_a = !GATHER && (u.rank == 0 || tl.rows > BM);
-    const int a_ctas = GATHER ? 0 : CG == 2 && tl.rows > BM ? 2 : 1;
+    const bool load_a = u.rank == 0 || tl.rows > BM;
+    const int a_ctas = CG == 2 && tl.rows > BM ? 2 : 1;
     const uint32_t bytes = a_ctas * (small ? SMALL_ROWS * BK : A_BYTES) + (two ? 2 : 1) * SUB_BYTES;
     // this CTA's boxes of W: gate and up, or two neighbouring boxes; of a pair, each CTA one
     const int row0 = OUT == OUT_SITU ? tl.n * SUB : tl.n * 2 * SUB;
@@ -174,8 +164,7 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
     }
   }
   // every load issued has landed before the block exits (a pair's loads land on
-  // the leader's barriers).  After an abort a stage may lack other arrivals:
-  // then the cap ends the wait.
+  // the leader's barriers).
   if (u.rank == 0)
     for (int i = 0; i < C::STAGES; ++i)
       if (issued & (1u << i)) {
@@ -187,7 +176,7 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
 // Scale words of four K blocks of a tile: of 128 rows of A, four per lane (rows
 // lane + 32 j), and of the two weight blocks.
 struct ScaleRows {
-  int row[4];   // rows of A, -1: none (its product is not stored, or of zeros)
+  int row[4];   // rows of A, -1: none (its product is not stored)
   int64_t at;   // first word of the weight block (SiTU: in both matrices)
   int second;   // words from there to the second block's
 };
@@ -203,15 +192,14 @@ __device__ __forceinline__ ScaleRows scale_rows(const Params& p, const Tile& tl)
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int i = lane + 32 * j;
-    if (i < tl.rows) r.row[j] = gathers<OUT, CG>() ? p.index[tl.m0 + i] : tl.m0 + i;
-    if (r.row[j] >= p.a_rows) r.row[j] = -1;
+    if (i < tl.rows) r.row[j] = tl.m0 + i;
   }
   return r;
 }
 template <int OUT>
 __device__ __forceinline__ ScaleWords scale_words(const Params& p, const ScaleRows& r, int q) {
   ScaleWords w{{0, 0, 0, 0}, 0, 0};
-  const uint32_t* a = p.a_words + (int64_t)q * p.a_rows;
+  const uint32_t* a = p.a_words + (int64_t)q * p.rows;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (r.row[j] >= 0) w.a[j] = a[r.row[j]];
@@ -219,112 +207,45 @@ __device__ __forceinline__ ScaleWords scale_words(const Params& p, const ScaleRo
   w.b1 = OUT == OUT_SITU ? p.w_up_words[r.at + q] : p.w_words[r.at + r.second + q];
   return w;
 }
-// The four row warps.  Scales: warp w writes the words to TMEM lanes 32 w ...:
-// columns 0-3 the words of rows 0-31, 32-63, 64-95 and 96-127 of A, 4-7 and
-// 8-11 those of the two weight blocks (one word for their 128 rows), the same in
-// each quarter, as the block-scaled MMA reads them.  Words, row numbers and
-// tiles are loaded one step ahead.
-// Rows of A by index (GATHER), 32 per warp: 16-byte asynchronous copies into the
-// swizzled layout a TMA load would leave.  (TMA's own gather of four rows took
-// about 100 cycles an instruction.)  Every copy reads inside its row, so that
-// none needs zero-filling: columns past n_in repeat the last ones (they meet
-// zeros of W), rows past the tile repeat its last row (never stored), and an
-// index outside A reads row 0 (its scale words are 0, and so is its product).
-// A stage of A is announced once its copies have landed; up to IN_FLIGHT stages
-// stay in flight, but none while the ring is full, when the tensor cores may be
-// waiting for exactly these.
-constexpr int IN_FLIGHT = 2, COPIES = 32 / ROW_WARPS;
+// Scale warp w writes the words to TMEM lanes 32 w ...: columns 0-3 the words of
+// rows 0-31, 32-63, 64-95 and 96-127 of A, 4-7 and 8-11 those of the two weight
+// blocks (one word for their 128 rows), the same in each quarter, as the
+// block-scaled MMA reads them.  Words and tiles are loaded one step ahead.
 template <int OUT, int CG>
-__device__ void feed_rows(const Params& p, uint32_t ring, uint32_t tmem, Sync& s, Unit u) {
-  using C = Cfg<CG>;
-  constexpr bool GATHER = gathers<OUT, CG>();
-  const int lane = threadIdx.x & 31, first = threadIdx.x & 96;
-  const int chunk = lane & 7, row0 = first + (lane >> 3);
+__device__ void feed_scales(const Params& p, uint32_t tmem, Sync& s, Unit u) {
+  const int lane = threadIdx.x & 31;
   const int total = total_tiles<CG>(p);
-  const uint32_t sfull0 = CG == 1 ? smem_u32(s.sfull) : map_to_rank(smem_u32(s.sfull), 0);
-  const uint32_t full0 = smem_u32(s.full), sf0 = tmem + SF_COL0 + ((uint32_t)first << 16);
-  int sstage = 0, stage = 0, head = 0;  // next scale stage, next stage, oldest stage in flight
-  uint32_t sphase = 0, phase = 0;
-  int flying = 0;
-  bool ok = true;
-  auto announce = [&]() {  // the oldest stage in flight, once it has landed
-    if (flying == 1) cp_async_wait<0>();
-    else if (flying == 2) cp_async_wait<1>();
-    else cp_async_wait<2>();
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full0 + 8 * head);
-    if (++head == C::STAGES) head = 0;
-    --flying;
-  };
-  Tile tl = own_rows<CG>(tile_ahead<CG>(p, u.first, total), u.rank);
+  const uint32_t full0 = CG == 1 ? smem_u32(s.sfull) : map_to_rank(smem_u32(s.sfull), 0);
+  const uint32_t sf0 = tmem + SF_COL0 + ((threadIdx.x & 96) << 16);
+  int stage = 0;
+  uint32_t phase = 0;
   Tile tn = own_rows<CG>(tile_ahead<CG>(p, u.first + u.step, total), u.rank);
-  ScaleRows rows = scale_rows<OUT, CG>(p, tl);
+  ScaleRows rows = scale_rows<OUT, CG>(p, own_rows<CG>(tile_ahead<CG>(p, u.first, total), u.rank));
   ScaleWords next = scale_words<OUT>(p, rows, 0);
-  for (int t = u.first; ok && t < total; t += u.step) {
-    uint32_t at[COPIES];  // rows of A, in 16-byte chunks
-    if (GATHER) {
-#pragma unroll
-      for (int i = 0; i < COPIES; ++i) {
-        const int r = min(row0 + 4 * i, tl.rows - 1);
-        uint32_t row = r >= 0 ? (uint32_t)p.index[tl.m0 + r] : 0u;
-        if (row >= (uint32_t)p.a_rows) row = 0;
-        at[i] = row * (uint32_t)(p.n_in >> 4);
-      }
-    }
+  for (int t = u.first; t < total; t += u.step) {
     const ScaleRows rows1 = scale_rows<OUT, CG>(p, tn);
-    for (int kb = 0; kb < p.kb; kb += GATHER ? 1 : 4) {
-      if (!GATHER || (kb & 3) == 0) {
-        const ScaleWords w = next;
-        const int q = (kb >> 2) + 1;
-        if (q == p.words) rows = rows1;
-        next = scale_words<OUT>(p, rows, q < p.words ? q : 0);
-        ok = warp_wait(smem_u32(&s.sempty[sstage]), sphase ^ 1u, &s.abort_flag, p.status);
-        if (!ok) break;
-        fence_after();
-        const uint32_t v[16] = {w.a[0], w.a[1], w.a[2], w.a[3], w.b0, w.b0, w.b0, w.b0,
-                                w.b1,   w.b1,   w.b1,   w.b1,   0,    0,    0,    0};
-        st16(sf0 + sstage * SF_COLS, v);
-        fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 1) mbar_arrive(sfull0 + 8 * sstage);
-          else mbar_arrive_remote(sfull0 + 8 * sstage);
-        }
-        if (++sstage == SF_STAGES) {
-          sstage = 0;
-          sphase ^= 1u;
-        }
+    tn = own_rows<CG>(tile_ahead<CG>(p, t + 2 * u.step, total), u.rank);
+    for (int q = 0; q < p.words; ++q) {
+      const ScaleWords w = next;
+      if (q + 1 == p.words) rows = rows1;
+      next = scale_words<OUT>(p, rows, q + 1 < p.words ? q + 1 : 0);
+      if (!warp_wait(smem_u32(&s.sempty[stage]), phase ^ 1u, &s.abort_flag, p.status)) return;
+      fence_after();
+      const uint32_t v[16] = {w.a[0], w.a[1], w.a[2], w.a[3], w.b0, w.b0, w.b0, w.b0,
+                              w.b1,   w.b1,   w.b1,   w.b1,   0,    0,    0,    0};
+      st16(sf0 + stage * SF_COLS, v);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1) mbar_arrive(full0 + 8 * stage);
+        else mbar_arrive_remote(full0 + 8 * stage);
       }
-      if (GATHER) {
-        const uint32_t empty = smem_u32(&s.empty[stage]);
-        while (flying > 0 && (flying > IN_FLIGHT ||
-                              !__all_sync(0xffffffffu, mbar_test(empty, phase ^ 1u))))
-          announce();
-        ok = warp_wait(empty, phase ^ 1u, &s.abort_flag, p.status);
-        if (!ok) break;
-        const uint32_t dst = ring + stage * C::STAGE_BYTES + row0 * BK;
-        const uint32_t col = min(kb * (BK / 16) + chunk, (p.n_in >> 4) - 1);
-        // row0 + 4 i: its last three bits alternate between two values
-        const uint32_t dst0 = dst + ((chunk ^ (row0 & 7)) << 4);
-        const uint32_t dst1 = dst + 4 * BK + ((chunk ^ ((row0 + 4) & 7)) << 4);
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i)
-          if (first + 4 * i < tl.rows)
-            cp_async16((i & 1 ? dst1 : dst0) + (i >> 1) * 8 * BK, p.a + (uint64_t)(at[i] + col) * 16);
-        cp_async_commit();
-        ++flying;
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      if (++stage == SF_STAGES) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
-    tl = tn;
-    tn = own_rows<CG>(tile_ahead<CG>(p, t + 2 * u.step, total), u.rank);
   }
-  if (!ok) cp_async_wait<0>();
-  while (ok && flying > 0) announce();
 }
 
 // The whole warp walks the tiles, so that addresses and descriptors stay in
@@ -654,11 +575,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                          : Unit{(int)(blockIdx.x >> 1), (int)(gridDim.x >> 1), (int)cluster_rank()};
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1 + (gathers<OUT, CG>() ? ROW_WARPS : 0));
+      mbar_init(smem_u32(&s.full[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < SF_STAGES; ++i) {
-      mbar_init(smem_u32(&s.sfull[i]), CG * ROW_WARPS);
+      mbar_init(smem_u32(&s.sfull[i]), CG * SCALE_WARPS);
       mbar_init(smem_u32(&s.sempty[i]), 1);
     }
     mbar_init(smem_u32(&s.tfull), 1);
@@ -685,12 +606,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
       if (u.rank == 0) issue_mmas<OUT, CG>(p, ring, tmem, s, u);
     }
-  } else if (warp < ROW_WARP0) {
+  } else if (warp < SCALE_WARP0) {
     regs_inc<REGS_EPI>();
     epilogue<OUT, CG>(p, tmem, staging, s, u);
   } else {
     regs_dec<REGS_OTHER>();
-    feed_rows<OUT, CG>(p, ring, tmem, s, u);
+    feed_scales<OUT, CG>(p, tmem, s, u);
   }
 
   fence_before();
@@ -781,20 +702,14 @@ cudaError_t launch(const Params& p, bool pairs, int64_t max_tiles, cudaStream_t 
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st) {
   if (g.rows == 0) return cudaSuccess;
   Params p{};
-  const bool gather = g.situ && !g.pairs;
-  if (gather != (g.index != nullptr)) return cudaErrorInvalidValue;
-  bool ok = (gather || (make_map(&p.tmA, g.a, g.n_in, g.a_rows, 1, BM, 2) &&
-                        make_map(&p.tmA32, g.a, g.n_in, g.a_rows, 1, SMALL_ROWS, 2))) &&
+  bool ok = make_map(&p.tmA, g.a, g.n_in, g.rows, 1, BM, 2) &&
+            make_map(&p.tmA32, g.a, g.n_in, g.rows, 1, SMALL_ROWS, 2) &&
             make_map(&p.tmB0, g.w, g.n_in, g.n_out, g.R, SUB, 3) &&
             (!g.situ || make_map(&p.tmB1, g.w_up, g.n_in, g.n_out, g.R, SUB, 3));
   if (!ok) return cudaErrorInvalidValue;
   p.a_words = reinterpret_cast<const uint32_t*>(g.a_scales);
   p.w_words = reinterpret_cast<const uint32_t*>(g.w_scales);
   p.w_up_words = reinterpret_cast<const uint32_t*>(g.w_up_scales);
-  p.a = g.a;
-  p.n_in = g.n_in;
-  p.index = g.index;
-  p.a_rows = (int)g.a_rows;
   p.rows = (int)g.rows;
   p.words = q_words(g.n_in);
   p.w_blocks = q_blocks(g.n_out);

@@ -45,13 +45,8 @@ cudaError_t launch_expert_tiles(const TileList& t, cudaStream_t st);
 
 // out [rows, n_out] = rows of a against the weights of the tile's expert.
 struct Fp8Gemm {
-  const uint8_t* a;         // [a_rows, n_in]
-  const uint8_t* a_scales;  // [words, a_rows, 4]
-  int64_t a_rows;
-  // with index, row r of the product is a[index[r]] (zeros outside [0, a_rows));
-  // without, a[r] and a_rows = rows.  SiTU on single CTAs needs it, the others
-  // do not take it.
-  const int32_t* index;
+  const uint8_t* a;         // [rows, n_in]
+  const uint8_t* a_scales;  // [words, rows, 4]
   int64_t rows;
   int R, n_in, n_out;
   const uint8_t* w;         // [R, n_out, n_in]

@@ -55,19 +55,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
         : "memory");
   return ok != 0;
 }
-// Whether the phase is over, without waiting (a try_wait may suspend the thread
-// for a while before it answers no).
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // Capped wait: false if the cap ran out (status recorded) or another role aborted.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
@@ -121,10 +108,9 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
                    "memory");
 }
-// Arrives on the barrier at a cluster address, ordering no memory accesses of
-// its own: for what was read from or written to TMEM (ordered by
-// tcgen05.fence), or to shared memory and already visible to the async proxy.
-// (A release at cluster scope took some 1500 cycles.)
+// Arrives on the barrier at a cluster address, ordering no memory accesses: for
+// what was read from or written to TMEM, which tcgen05.fence orders.  (A release
+// at cluster scope took some 1500 cycles.)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
@@ -160,18 +146,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
-// 16 bytes of global memory to shared memory, past L1.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>  // all but the last N groups have landed
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Registers of a thread of this warpgroup (every warp of it calls this).
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -187,11 +161,6 @@ __device__ __forceinline__ void fence_before() {
 }
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// Shared-memory writes of this thread become visible to the async proxy
-// (tcgen05 reads through it).
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 // Arrive, when this thread's MMAs are complete, on the barrier at this offset
 // (CG = 2: in both CTAs of the pair).
