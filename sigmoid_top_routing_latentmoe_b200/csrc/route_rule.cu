@@ -8,6 +8,7 @@
 // Ties go to the lower group and the lower expert; a key that is NaN ranks
 // with -inf, so that every row has k distinct experts.  b only selects.
 #include <algorithm>
+#include <cfloat>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -27,6 +28,10 @@ __device__ __forceinline__ uint32_t key_code(float f) {
   if (isnan(f)) f = -INFINITY;
   const uint32_t u = __float_as_uint(f + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+// The key of a code (0 for -0).
+__device__ __forceinline__ float decode_key(uint32_t c) {
+  return __uint_as_float((c & 0x80000000u) ? c & 0x7fffffffu : ~c);
 }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -53,19 +58,32 @@ __device__ __forceinline__ uint32_t warp_sort_desc(uint32_t v) {
   return v;
 }
 
-// Groups of experts in shared memory, per warp: the keys (a padding of `pad`
+// The keys are formed with the fast exponential and reciprocal (off by a few
+// 2^-24, as any 32-bit form is; equal logits give equal keys), the weights of
+// the chosen experts with expf and a division.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Groups of experts in shared memory, per warp: the keys (a padding of `lanes`
 // floats after each group keeps the lanes that share a group's scan on
 // different banks), the groups' codes, and a bit per kept group.
 struct Groups {
   int n, kept, size, lanes, top2;  // lanes: how many lanes scan one group (a power of two)
-  float inv_size;
+  uint32_t magic;                  // ceil(2^32 / size): e / size = umulhi(e, magic) for e < 4096
   __host__ __device__ int key_words() const { return n * (size + lanes); }
   __host__ __device__ int words() const { return key_words() + n + (n + 31) / 32; }
 };
-// Group of expert e: (e + 1/2) / size lies at least 1 / (2 size) from a whole
-// number, the rounding of the product below 1e-3 / size (e < 4096).
 __device__ __forceinline__ int group_of(const Groups& g, int e) {
-  return (int)(((float)e + 0.5f) * g.inv_size);
+  return g.size == 1 ? e : (int)__umulhi((uint32_t)e, g.magic);
 }
 
 // Marks the topk_groups best groups in the warp's bits.
@@ -84,14 +102,16 @@ __device__ __forceinline__ const uint32_t* keep_groups(const Groups& g, const fl
   const int per = 32 / g.lanes, sub = lane & (g.lanes - 1);
   for (int g0 = 0; g0 < g.n; g0 += per) {
     const int gi = g0 + lane / g.lanes;
-    float a = -INFINITY, b = -INFINITY;  // the two largest keys
-    if (gi < g.n)
-      for (int i = sub; i < g.size; i += g.lanes) {
-        float v = sm[gi * (g.size + g.lanes) + i];
-        if (isnan(v)) v = -INFINITY;
+    float a = -INFINITY, b = -INFINITY;  // the two largest keys (a NaN counts as -inf)
+    if (gi < g.n) {
+      const float* k = sm + gi * (g.size + g.lanes) + sub;
+#pragma unroll 8
+      for (int i = 0; i < g.size - sub; i += g.lanes) {
+        const float v = fmaxf(k[i], -INFINITY);
         b = fmaxf(b, fminf(a, v));
         a = fmaxf(a, v);
       }
+    }
     for (int off = g.lanes >> 1; off > 0; off >>= 1) {
       const float oa = __shfl_xor_sync(kAll, a, off), ob = __shfl_xor_sync(kAll, b, off);
       b = fmaxf(fminf(a, oa), fmaxf(b, ob));
@@ -106,6 +126,7 @@ __device__ __forceinline__ const uint32_t* keep_groups(const Groups& g, const fl
     if (gi < g.n) {
       const uint32_t c = code[gi];
       rank = 0;
+#pragma unroll 4
       for (int o = 0; o < g.n; ++o) rank += code[o] > c || (code[o] == c && o < gi);
     }
     const uint32_t m = __ballot_sync(kAll, rank < g.kept);
@@ -115,11 +136,39 @@ __device__ __forceinline__ const uint32_t* keep_groups(const Groups& g, const fl
   return bits;
 }
 
+// The k largest codes of those held VPL per lane (expert j * 32 + lane; 0: not
+// to be chosen), in k rounds of two warp reductions; lane `slot` of each 32
+// slots gets the slot's expert, which `done` writes.
+template <int VPL, typename Done>
+__device__ __forceinline__ void select_rounds(uint32_t (&code)[VPL], int k, Done done) {
+  const int lane = threadIdx.x & 31;
+  for (int base = 0; base < k; base += 32) {
+    const int slots = min(32, k - base);
+    int chosen = 0;
+    for (int slot = 0; slot < slots; ++slot) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) best = max(best, code[j]);
+      const uint32_t m = __reduce_max_sync(kAll, best);
+      int at = 0x7fffffff;
+#pragma unroll
+      for (int j = VPL - 1; j >= 0; --j)
+        if (code[j] == m) at = j * 32 + lane;
+      const int e = __reduce_min_sync(kAll, at);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (j * 32 + lane == e) code[j] = 0;
+      if (slot == lane) chosen = e;
+    }
+    done(base, slots, chosen);
+  }
+}
+
 // One warp per token; expert j * 32 + lane is value j of the lane.
 // k <= 32 of many experts: the k-th largest of the 32 lane maxima bounds the
 // k-th largest key from below, so only the keys at or above it (a few dozen)
-// go into the k rounds of selection, two per lane.  Clustered keys (more than
-// 64 above the bound) and k > 32 take the rounds over every key.
+// are put in order, each by counting the ones before it.  Clustered keys (more
+// than 64 above the bound), k > 32 and R <= 64 take k rounds of a warp maximum.
 template <int VPL, bool SOFTMAX>
 __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     const float* __restrict__ logits, int64_t ld, const float* __restrict__ bias, int64_t n, int R,
@@ -127,8 +176,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     float* __restrict__ probs) {
   pdl_trigger();
   pdl_wait();
-  __shared__ uint32_t cand_code[kWarps][64];
-  __shared__ int cand_e[kWarps][64];
+  __shared__ uint64_t cand[kWarps][64];  // code, then ~expert: the larger comes first
+  __shared__ int slot_e[kWarps][32];
   extern __shared__ float sm_keys[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
@@ -150,7 +199,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      key[j] = expf(key[j] - top);
+      key[j] = ex2((key[j] - top) * kLog2e);
       sum += key[j];
     }
     sum = warp_sum(sum);
@@ -159,101 +208,33 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const int e = j * 32 + lane;
-    const float s = SOFTMAX ? key[j] * inv : sigmoid_f(key[j]);
+    const float s = SOFTMAX ? key[j] * inv : rcp(1.0f + ex2(-kLog2e * key[j]));
     key[j] = s + (bias != nullptr && e < R ? bias[e] : 0.0f);
   }
+  uint32_t closed = 0;  // bit j: value j is not to be chosen (VPL > 32: found again below)
   const uint32_t* bits = nullptr;
   if (g.kept < g.n) bits = keep_groups<VPL>(g, key, R, sm_keys + warp * g.words());
-  uint32_t code[VPL];  // 0: not to be chosen
-  uint32_t lmax = 0;
+  auto is_open = [&](int j) {
+    const int e = j * 32 + lane;
+    if (e >= R) return false;
+    if (bits == nullptr) return true;
+    const int gi = group_of(g, e);
+    return ((bits[gi >> 5] >> (gi & 31)) & 1u) != 0;
+  };
+  float lmax = -INFINITY;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const int e = j * 32 + lane;
-    bool open = e < R;
-    if (open && bits != nullptr) {
-      const int gi = group_of(g, e);
-      open = (bits[gi >> 5] >> (gi & 31)) & 1u;
-    }
-    code[j] = open ? key_code(key[j]) : 0u;
-    lmax = max(lmax, code[j]);
+    const bool open = is_open(j);
+    if (VPL <= 32 && !open) closed |= 1u << (j & 31);
+    if (open) lmax = fmaxf(lmax, fmaxf(key[j], -FLT_MAX));
   }
-  // candidates: two codes per lane, or all of them
-  uint32_t c0 = 0, c1 = 0;
-  int e0 = 0, e1 = 0;
-  bool few = VPL <= 2;
-  if (VPL <= 2) {
-    c0 = code[0];
-    e0 = lane;
-    if (VPL == 2) {
-      c1 = code[VPL - 1];
-      e1 = 32 + lane;
-    }
-  } else if (k <= 32) {
-    const uint32_t least = max(1u, __shfl_sync(kAll, warp_sort_desc(lmax), k - 1));
-    int mine = 0;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) mine += code[j] >= least ? 1 : 0;
-    int incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(kAll, incl, off);
-      if (lane >= off) incl += o;
-    }
-    const int total = __shfl_sync(kAll, incl, 31);
-    few = total <= 64;
-    if (few) {
-      int at = incl - mine;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (code[j] >= least) {
-          cand_code[warp][at] = code[j];
-          cand_e[warp][at++] = j * 32 + lane;
-        }
-      __syncwarp();
-      if (lane < total) {
-        c0 = cand_code[warp][lane];
-        e0 = cand_e[warp][lane];
-      }
-      if (lane + 32 < total) {
-        c1 = cand_code[warp][lane + 32];
-        e1 = cand_e[warp][lane + 32];
-      }
-    }
-  }
+  auto code_of = [&](int j) {
+    return (VPL <= 32 ? (closed >> (j & 31)) & 1u : !is_open(j)) ? 0u : key_code(key[j]);
+  };
   int32_t* ids_row = ids + t * k;
   float* probs_row = probs + t * k;
   float sum = 0.0f;
-  for (int base = 0; base < k; base += 32) {
-    const int slots = min(32, k - base);
-    int chosen = 0;
-    for (int slot = 0; slot < slots; ++slot) {
-      uint32_t best = max(c0, c1);
-      if (!few) {
-        best = 0;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) best = max(best, code[j]);
-      }
-      const uint32_t m = __reduce_max_sync(kAll, best);
-      int at = 0x7fffffff;
-      if (few) {
-        if (c0 == m) at = e0;
-        if (c1 == m) at = min(at, e1);
-      } else {
-#pragma unroll
-        for (int j = VPL - 1; j >= 0; --j)
-          if (code[j] == m) at = j * 32 + lane;
-      }
-      const int e = __reduce_min_sync(kAll, at);
-      if (few) {
-        if (e0 == e) c0 = 0;
-        if (e1 == e) c1 = 0;
-      } else {
-#pragma unroll
-        for (int j = 0; j < VPL; ++j)
-          if (j * 32 + lane == e) code[j] = 0;
-      }
-      if (slot == lane) chosen = e;
-    }
+  auto done = [&](int base, int slots, int chosen) {
     float s = 0.0f;
     if (lane < slots) {
       const float l = lr[chosen];
@@ -266,6 +247,54 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
       if (k <= 32) s = scale * (renormalise ? s / fmaxf(sum, kMinSum) : s);
       probs_row[base + lane] = s;
     }
+  };
+  int total = 65;
+  if (VPL > 2 && k <= 32) {
+    // keys of -inf and NaN count as the lowest finite ones here: a superset
+    const float least =
+        decode_key(max(1u, __shfl_sync(kAll, warp_sort_desc(key_code(lmax)), k - 1)));
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const bool open = VPL <= 32 ? !((closed >> (j & 31)) & 1u) : is_open(j);
+      mine += open && fmaxf(key[j], -FLT_MAX) >= least ? 1 : 0;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(kAll, incl, off);
+      if (lane >= off) incl += o;
+    }
+    total = __shfl_sync(kAll, incl, 31);
+    if (total <= 64) {
+      int at = incl - mine;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const bool open = VPL <= 32 ? !((closed >> (j & 31)) & 1u) : is_open(j);
+        if (open && fmaxf(key[j], -FLT_MAX) >= least)
+          cand[warp][at++] = (uint64_t)key_code(key[j]) << 32 | (uint32_t)~(j * 32 + lane);
+      }
+      __syncwarp();
+      const uint64_t c0 = lane < total ? cand[warp][lane] : 0;
+      const uint64_t c1 = lane + 32 < total ? cand[warp][lane + 32] : 0;
+      int r0 = 0, r1 = 0;
+#pragma unroll 4
+      for (int i = 0; i < total; ++i) {
+        const uint64_t c = cand[warp][i];
+        r0 += c > c0;
+        r1 += c > c1;
+      }
+      if (c0 != 0 && r0 < k) slot_e[warp][r0] = (int)~(uint32_t)c0;
+      if (c1 != 0 && r1 < k) slot_e[warp][r1] = (int)~(uint32_t)c1;
+      __syncwarp();
+      done(0, k, lane < k ? slot_e[warp][lane] : 0);
+    }
+  }
+  if (total > 64) {
+    uint32_t code[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) code[j] = code_of(j);
+    select_rounds<VPL>(code, k, done);
   }
   if (k > 32)  // each lane's own values
     for (int slot = lane; slot < k; slot += 32)
@@ -392,7 +421,7 @@ cudaError_t launch_route_rule(const RouteRule& rule, const float* logits, int64_
   g.lanes = 1;
   while (g.lanes * 2 * g.n <= 32) g.lanes *= 2;
   g.top2 = rule.top2;
-  g.inv_size = 1.0f / (float)g.size;
+  g.magic = g.size == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + g.size - 1) / g.size);
   LMOE_VPL_SWITCH(R, (rule.softmax ? launch_rule<kV, true>(rule, g, logits, ld, bias, n, R, k, ids,
                                                            probs, st)
                                    : launch_rule<kV, false>(rule, g, logits, ld, bias, n, R, k, ids,
