@@ -253,27 +253,56 @@ GROUP_TOP2, GROUP_MAX = 0, 1
 FP8 = torch.float8_e4m3fn
 
 
-def _want(where, name, t, shape, dtype, contiguous=True):
-    """Refuses a tensor that the C ABI would misread."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise LmoeError(EINVAL, where, f"{name}: expected a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise LmoeError(EINVAL, where, f"{name} is on {t.device}, not on the current device "
-                                       f"cuda:{torch.cuda.current_device()}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or (contiguous and not t.is_contiguous()):
-        raise LmoeError(EINVAL, where, f"{name}: expected a contiguous {dtype} tensor of shape "
-                                       f"{tuple(shape)}, got {t.dtype} of shape {tuple(t.shape)}, "
-                                       f"strides {t.stride()}")
+# The current stream's handle on a device, without building a Stream object
+# (a tenth of the time: these calls may be as short as a kernel launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _want_rows(where, name, t, n, cols):
-    """A float32 [n, cols] tensor whose rows are contiguous; returns its row stride."""
-    _want(where, name, t, (n, cols), torch.float32, contiguous=False)
+def _want(where, *tensors, stream=None):
+    """Refuses tensors that the C ABI would misread: each (name, tensor, shape, dtype) has to
+    be contiguous on the current device.  Returns the stream's handle."""
+    dev = None
+    for name, t, shape, dtype in tensors:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise LmoeError(EINVAL, where, f"{name}: expected a CUDA tensor")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise LmoeError(EINVAL, where, f"{name} is on {t.device}, not on the current device cuda:{dev}")
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise LmoeError(EINVAL, where, f"{name}: expected a contiguous {dtype} tensor of shape "
+                                           f"{tuple(shape)}, got {t.dtype} of shape {tuple(t.shape)}, "
+                                           f"strides {t.stride()}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _row_stride(where, name, t, shape, dtypes):
+    """Row stride of a matrix on the current device whose rows are contiguous and apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise LmoeError(EINVAL, where, f"{name}: expected a tensor on the current CUDA device")
+    if t.dtype not in dtypes or t.shape != shape:
+        raise LmoeError(EINVAL, where, f"{name}: expected {' or '.join(map(str, dtypes))} of shape "
+                                       f"{tuple(shape)}, got {t.dtype} of shape {tuple(t.shape)}")
+    n, cols = shape
+    if n <= 1:
+        ld = cols
+    else:
+        ld = t.stride(0)
+        if ld < cols:
+            raise LmoeError(EINVAL, where, f"{name}: rows overlap")
     if n > 0 and cols > 1 and t.stride(1) != 1:
         raise LmoeError(EINVAL, where, f"{name}: the columns of a row must be neighbours")
-    if n > 1 and t.stride(0) < cols:
-        raise LmoeError(EINVAL, where, f"{name}: rows overlap")
-    return t.stride(0) if n > 1 else cols
+    return ld
+
+
+def _bias_spec(expert_bias, n):
+    return [] if expert_bias is None else [("expert_bias", expert_bias, (n,), torch.float32)]
+
+
+def _act(dims):
+    return torch.bfloat16 if dims.dtype == BF16 else torch.float32
 
 
 def make_route_rule(score=SCORE_SIGMOID, n_groups=1, topk_groups=1, group_score=GROUP_TOP2,
@@ -285,43 +314,34 @@ def moe_route_grouped(dims, rule, x, w_router, expert_bias, ids, probs, ws, stre
     """moe_route under a rule with groups of experts (make_route_rule)."""
     where, act = "moe_route_grouped", _act(dims)
     N, R, k = dims.n_tokens, dims.n_routed, dims.top_k
-    _want(where, "x", x, (N, dims.d), act)
-    _want(where, "w_router", w_router, (R, dims.d), act)
-    if expert_bias is not None:
-        _want(where, "expert_bias", expert_bias, (R,), torch.float32)
-    _want(where, "ids", ids, (N, k), torch.int32)
-    _want(where, "probs", probs, (N, k), torch.float32)
+    st = _want(where, ("x", x, (N, dims.d), act), ("w_router", w_router, (R, dims.d), act),
+               ("ids", ids, (N, k), torch.int32), ("probs", probs, (N, k), torch.float32),
+               *_bias_spec(expert_bias, R), stream=stream)
     _check(_lib.moe_route_grouped(ctypes.byref(dims), ctypes.byref(rule), _ptr(x), _ptr(w_router),
                                   _ptr(expert_bias), _ptr(ids), _ptr(probs), _ptr(ws), ws.numel(),
-                                  _stream(stream)), where)
+                                  st), where)
 
 
 def moe_route_logits(dims, rule, logits, expert_bias, ids, probs, stream=None):
     """The same from given float32 logits [N, R] (any row stride)."""
     where, N, R, k = "moe_route_logits", dims.n_tokens, dims.n_routed, dims.top_k
-    ld = _want_rows(where, "logits", logits, N, R)
-    if expert_bias is not None:
-        _want(where, "expert_bias", expert_bias, (R,), torch.float32)
-    _want(where, "ids", ids, (N, k), torch.int32)
-    _want(where, "probs", probs, (N, k), torch.float32)
+    ld = _row_stride(where, "logits", logits, (N, R), (torch.float32,))
+    st = _want(where, ("ids", ids, (N, k), torch.int32), ("probs", probs, (N, k), torch.float32),
+               *_bias_spec(expert_bias, R), stream=stream)
     _check(_lib.moe_route_logits(ctypes.byref(dims), ctypes.byref(rule), _ptr(logits), ld,
-                                 _ptr(expert_bias), _ptr(ids), _ptr(probs), _stream(stream)), where)
+                                 _ptr(expert_bias), _ptr(ids), _ptr(probs), st), where)
 
 
 def moe_route_logits_backward(dims, rule, logits, ids, dprobs, dlogits, stream=None):
-    """dlogits [N, R] <- the gradient of <dprobs, probs> with respect to the logits."""
+    """dlogits [N, R] <- the gradient of <dprobs, probs> with respect to the logits (both of any
+    row stride)."""
     where, N, R, k = "moe_route_logits_backward", dims.n_tokens, dims.n_routed, dims.top_k
-    ld = _want_rows(where, "logits", logits, N, R)
-    ldd = _want_rows(where, "dlogits", dlogits, N, R)
-    _want(where, "ids", ids, (N, k), torch.int32)
-    _want(where, "dprobs", dprobs, (N, k), torch.float32)
+    ld = _row_stride(where, "logits", logits, (N, R), (torch.float32,))
+    ldd = _row_stride(where, "dlogits", dlogits, (N, R), (torch.float32,))
+    st = _want(where, ("ids", ids, (N, k), torch.int32), ("dprobs", dprobs, (N, k), torch.float32),
+               stream=stream)
     _check(_lib.moe_route_logits_backward(ctypes.byref(dims), ctypes.byref(rule), _ptr(logits), ld,
-                                          _ptr(ids), _ptr(dprobs), _ptr(dlogits), ldd,
-                                          _stream(stream)), where)
-
-
-def _act(dims):
-    return torch.bfloat16 if dims.dtype == BF16 else torch.float32
+                                          _ptr(ids), _ptr(dprobs), _ptr(dlogits), ldd, st), where)
 
 
 def fp8_row_scales_shape(rows: int, cols: int) -> tuple:
@@ -334,76 +354,72 @@ def fp8_weight_scales_shape(mats: int, rows: int, cols: int) -> tuple:
     return (mats, (rows + 127) // 128, 4 * ((cols + 511) // 512))
 
 
+def _matrix_dims(where, name, t, n):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise LmoeError(EINVAL, where, f"{name}: expected a tensor of {n} dimensions")
+    return t.shape
+
+
 def quantize_rows_fp8(x, q, scales, index=None, stream=None):
     """q [n, c] e4m3, scales <- the rows of x (bfloat16 or float32, any row stride that is
     a multiple of 16 bytes), or x[index] with int32 index [n]."""
     where = "quantize_rows_fp8"
-    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
-        raise LmoeError(EINVAL, where, "x: expected a bfloat16 or float32 matrix")
-    n_src, cols = x.shape
-    _want(where, "x", x, (n_src, cols), x.dtype, contiguous=False)
-    if n_src > 0 and cols > 1 and x.stride(1) != 1:
-        raise LmoeError(EINVAL, where, "x: the columns of a row must be neighbours")
-    n = n_src
-    if index is not None:
-        n = index.numel()
-        _want(where, "index", index, (n,), torch.int32)
-    _want(where, "q", q, (n, cols), FP8)
-    _want(where, "scales", scales, fp8_row_scales_shape(n, cols), torch.uint8)
-    _check(_lib.lmoe_quantize_rows_fp8(_ptr(x), BF16 if x.dtype == torch.bfloat16 else F32, n_src,
-                                       x.stride(0) if n_src > 1 else cols, _ptr(index), n, cols,
-                                       _ptr(q), _ptr(scales), _stream(stream)), where)
+    n_src, cols = _matrix_dims(where, "x", x, 2)
+    ld = _row_stride(where, "x", x, (n_src, cols), (torch.bfloat16, torch.float32))
+    n = n_src if index is None else index.numel()
+    st = _want(where, ("q", q, (n, cols), FP8),
+               ("scales", scales, fp8_row_scales_shape(n, cols), torch.uint8),
+               *([] if index is None else [("index", index, (n,), torch.int32)]), stream=stream)
+    _check(_lib.lmoe_quantize_rows_fp8(_ptr(x), BF16 if x.dtype is torch.bfloat16 else F32, n_src,
+                                       ld, _ptr(index), n, cols, _ptr(q), _ptr(scales), st), where)
 
 
 def quantize_weights_fp8(w, q, scales, stream=None):
     """q, scales <- the stacked matrices w [m, r, c] (bfloat16 or float32)."""
     where = "quantize_weights_fp8"
-    if w.dim() != 3 or w.dtype not in (torch.bfloat16, torch.float32):
-        raise LmoeError(EINVAL, where, "w: expected stacked bfloat16 or float32 matrices")
-    m, r, c = w.shape
-    _want(where, "w", w, (m, r, c), w.dtype)
-    _want(where, "q", q, (m, r, c), FP8)
-    _want(where, "scales", scales, fp8_weight_scales_shape(m, r, c), torch.uint8)
-    _check(_lib.lmoe_quantize_weights_fp8(_ptr(w), BF16 if w.dtype == torch.bfloat16 else F32, m, r,
-                                          c, _ptr(q), _ptr(scales), _stream(stream)), where)
+    m, r, c = _matrix_dims(where, "w", w, 3)
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise LmoeError(EINVAL, where, "w: expected bfloat16 or float32")
+    st = _want(where, ("w", w, w.shape, w.dtype), ("q", q, (m, r, c), FP8),
+               ("scales", scales, fp8_weight_scales_shape(m, r, c), torch.uint8), stream=stream)
+    _check(_lib.lmoe_quantize_weights_fp8(_ptr(w), BF16 if w.dtype is torch.bfloat16 else F32, m, r,
+                                          c, _ptr(q), _ptr(scales), st), where)
 
 
 def moe_expert_gemm_fp8(dims, a, a_scales, offsets, w, w_scales, out, ws, stream=None):
     """out [N*k, n_out] <- quantised rows a times the quantised weights w [R, n_out, n_in] of
     their expert (offsets=None: one expert that has every row)."""
     where, P, R = "moe_expert_gemm_fp8", dims.n_tokens * dims.top_k, dims.n_routed
-    if not isinstance(w, torch.Tensor) or w.dim() != 3:
-        raise LmoeError(EINVAL, where, "w: expected stacked matrices")
-    n_out, n_in = w.shape[1:]
-    _want(where, "a", a, (P, n_in), FP8)
-    _want(where, "a_scales", a_scales, fp8_row_scales_shape(P, n_in), torch.uint8)
-    if offsets is not None:
-        _want(where, "offsets", offsets, (R + 1,), torch.int32)
-    _want(where, "w", w, (R, n_out, n_in), FP8)
-    _want(where, "w_scales", w_scales, fp8_weight_scales_shape(R, n_out, n_in), torch.uint8)
-    _want(where, "out", out, (P, n_out), _act(dims))
+    _, n_out, n_in = _matrix_dims(where, "w", w, 3)
+    st = _want(where, ("a", a, (P, n_in), FP8),
+               ("a_scales", a_scales, fp8_row_scales_shape(P, n_in), torch.uint8),
+               ("w", w, (R, n_out, n_in), FP8),
+               ("w_scales", w_scales, fp8_weight_scales_shape(R, n_out, n_in), torch.uint8),
+               ("out", out, (P, n_out), _act(dims)),
+               *([] if offsets is None else [("offsets", offsets, (R + 1,), torch.int32)]),
+               stream=stream)
     _check(_lib.moe_expert_gemm_fp8(ctypes.byref(dims), n_in, n_out, _ptr(a), _ptr(a_scales),
                                     _ptr(offsets), _ptr(w), _ptr(w_scales), _ptr(out), _ptr(ws),
-                                    ws.numel(), _stream(stream)), where)
+                                    ws.numel(), st), where)
 
 
 def moe_expert_ffn_fp8(dims, z, perm_token, offsets, w_g, w_g_scales, w_u, w_u_scales, w_o,
                        w_o_scales, expert_out, ws, stream=None):
     """moe_expert_ffn with quantised weights (quantize_weights_fp8)."""
     where, P, R = "moe_expert_ffn_fp8", dims.n_tokens * dims.top_k, dims.n_routed
-    L, F = dims.latent, dims.ff_routed
-    _want(where, "z", z, (dims.n_tokens, L), _act(dims))
-    _want(where, "perm_token", perm_token, (P,), torch.int32)
-    _want(where, "offsets", offsets, (R + 1,), torch.int32)
-    for name, w, s, r, c in (("w_g", w_g, w_g_scales, F, L), ("w_u", w_u, w_u_scales, F, L),
-                             ("w_o", w_o, w_o_scales, L, F)):
-        _want(where, name, w, (R, r, c), FP8)
-        _want(where, name + "_scales", s, fp8_weight_scales_shape(R, r, c), torch.uint8)
-    _want(where, "expert_out", expert_out, (P, L), _act(dims))
+    L, F, act = dims.latent, dims.ff_routed, _act(dims)
+    in_scales, out_scales = fp8_weight_scales_shape(R, F, L), fp8_weight_scales_shape(R, L, F)
+    st = _want(where, ("z", z, (dims.n_tokens, L), act),
+               ("perm_token", perm_token, (P,), torch.int32),
+               ("offsets", offsets, (R + 1,), torch.int32),
+               ("w_g", w_g, (R, F, L), FP8), ("w_g_scales", w_g_scales, in_scales, torch.uint8),
+               ("w_u", w_u, (R, F, L), FP8), ("w_u_scales", w_u_scales, in_scales, torch.uint8),
+               ("w_o", w_o, (R, L, F), FP8), ("w_o_scales", w_o_scales, out_scales, torch.uint8),
+               ("expert_out", expert_out, (P, L), act), stream=stream)
     ew = Fp8Experts(*[_ptr(t) for t in (w_g, w_g_scales, w_u, w_u_scales, w_o, w_o_scales)])
     _check(_lib.moe_expert_ffn_fp8(ctypes.byref(dims), _ptr(z), _ptr(perm_token), _ptr(offsets),
-                                   ctypes.byref(ew), _ptr(expert_out), _ptr(ws), ws.numel(),
-                                   _stream(stream)), where)
+                                   ctypes.byref(ew), _ptr(expert_out), _ptr(ws), ws.numel(), st),
+           where)
 
 
 def moe_combine(dims, expert_out, inv_pair, probs, rms_weight, u_normed, stream=None):

@@ -73,38 +73,27 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Groups of experts in shared memory, per warp: the keys (a padding of `lanes`
-// floats after each group keeps the lanes that share a group's scan on
-// different banks), the groups' codes, and a bit per kept group.
+// Shared memory of a warp: the keys, group by group (a padding of `lanes` floats
+// after each group keeps the lanes that share a group's scan on different
+// banks), the groups' codes and the kept groups in ascending order.
 struct Groups {
   int n, kept, size, lanes, top2;  // lanes: how many lanes scan one group (a power of two)
   uint32_t magic;                  // ceil(2^32 / size): e / size = umulhi(e, magic) for e < 4096
   __host__ __device__ int key_words() const { return n * (size + lanes); }
-  __host__ __device__ int words() const { return key_words() + n + (n + 31) / 32; }
+  __host__ __device__ int words() const { return key_words() + 2 * n; }
+  __device__ int group_of(int e) const { return size == 1 ? e : (int)__umulhi((uint32_t)e, magic); }
 };
-__device__ __forceinline__ int group_of(const Groups& g, int e) {
-  return g.size == 1 ? e : (int)__umulhi((uint32_t)e, g.magic);
-}
 
-// Marks the topk_groups best groups in the warp's bits.
-template <int VPL>
-__device__ __forceinline__ const uint32_t* keep_groups(const Groups& g, const float (&key)[VPL],
-                                                       int R, float* sm) {
+// Puts the topk_groups best groups in ascending order into `list`.
+__device__ __forceinline__ void keep_groups(const Groups& g, const float* key, uint32_t* code,
+                                            int* list) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e = j * 32 + lane;
-    if (e < R) sm[e + group_of(g, e) * g.lanes] = key[j];
-  }
-  uint32_t* code = reinterpret_cast<uint32_t*>(sm) + g.key_words();
-  uint32_t* bits = code + g.n;
-  __syncwarp();
   const int per = 32 / g.lanes, sub = lane & (g.lanes - 1);
   for (int g0 = 0; g0 < g.n; g0 += per) {
     const int gi = g0 + lane / g.lanes;
     float a = -INFINITY, b = -INFINITY;  // the two largest keys (a NaN counts as -inf)
     if (gi < g.n) {
-      const float* k = sm + gi * (g.size + g.lanes) + sub;
+      const float* k = key + gi * (g.size + g.lanes) + sub;
 #pragma unroll 8
       for (int i = 0; i < g.size - sub; i += g.lanes) {
         const float v = fmaxf(k[i], -INFINITY);
@@ -120,6 +109,7 @@ __device__ __forceinline__ const uint32_t* keep_groups(const Groups& g, const fl
     if (gi < g.n && sub == 0) code[gi] = key_code(g.top2 && g.size > 1 ? a + b : a);
   }
   __syncwarp();
+  int kept = 0;
   for (int g0 = 0; g0 < g.n; g0 += 32) {
     const int gi = g0 + lane;
     int rank = g.kept;
@@ -130,111 +120,112 @@ __device__ __forceinline__ const uint32_t* keep_groups(const Groups& g, const fl
       for (int o = 0; o < g.n; ++o) rank += code[o] > c || (code[o] == c && o < gi);
     }
     const uint32_t m = __ballot_sync(kAll, rank < g.kept);
-    if (lane == 0) bits[g0 >> 5] = m;
+    if (rank < g.kept) list[kept + __popc(m & ((1u << lane) - 1u))] = gi;
+    kept += __popc(m);
   }
   __syncwarp();
-  return bits;
 }
 
-// The k largest codes of those held VPL per lane (expert j * 32 + lane; 0: not
-// to be chosen), in k rounds of two warp reductions; lane `slot` of each 32
-// slots gets the slot's expert, which `done` writes.
-template <int VPL, typename Done>
-__device__ __forceinline__ void select_rounds(uint32_t (&code)[VPL], int k, Done done) {
-  const int lane = threadIdx.x & 31;
-  for (int base = 0; base < k; base += 32) {
-    const int slots = min(32, k - base);
-    int chosen = 0;
-    for (int slot = 0; slot < slots; ++slot) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) best = max(best, code[j]);
-      const uint32_t m = __reduce_max_sync(kAll, best);
-      int at = 0x7fffffff;
-#pragma unroll
-      for (int j = VPL - 1; j >= 0; --j)
-        if (code[j] == m) at = j * 32 + lane;
-      const int e = __reduce_min_sync(kAll, at);
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (j * 32 + lane == e) code[j] = 0;
-      if (slot == lane) chosen = e;
-    }
-    done(base, slots, chosen);
-  }
-}
+constexpr uint32_t kTaken = 0xffffffffu;  // bits of a key that has its slot
 
-// One warp per token; expert j * 32 + lane is value j of the lane.
-// k <= 32 of many experts: the k-th largest of the 32 lane maxima bounds the
-// k-th largest key from below, so only the keys at or above it (a few dozen)
-// are put in order, each by counting the ones before it.  Clustered keys (more
-// than 64 above the bound), k > 32 and R <= 64 take k rounds of a warp maximum.
-template <int VPL, bool SOFTMAX>
+// One warp per token; its keys stay in shared memory, so that the groups may
+// have any size and the registers go to warps in flight.
+// With k <= 32 and more than 64 open experts, the k-th largest of the 32 lane
+// maxima bounds the k-th largest key from below, so only the keys at or above
+// it (a few dozen) are put in order: each by counting the ones before it, or in
+// k rounds of a warp maximum where k is small.  Clustered keys (more than 64
+// above the bound) and k > 32 take the rounds over every open key.
+template <bool SOFTMAX>
 __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     const float* __restrict__ logits, int64_t ld, const float* __restrict__ bias, int64_t n, int R,
     int k, Groups g, int renormalise, float scale, int32_t* __restrict__ ids,
     float* __restrict__ probs) {
   pdl_trigger();
   pdl_wait();
-  __shared__ uint64_t cand[kWarps][64];  // code, then ~expert: the larger comes first
-  __shared__ int slot_e[kWarps][32];
-  extern __shared__ float sm_keys[];
+  __shared__ uint64_t cands[kWarps][64];  // code, then ~expert: the larger comes first
+  __shared__ int slots_e[kWarps][32];
+  extern __shared__ float sm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
   if (t >= n) return;
   const float* lr = logits + t * ld;
-  float key[VPL];
+  float* key = sm + warp * g.words();
+  uint32_t* code = reinterpret_cast<uint32_t*>(key + g.key_words());
+  int* list = reinterpret_cast<int*>(code + g.n);
+  uint64_t* cand = cands[warp];
+  int* slot_e = slots_e[warp];
+  const bool grouped = g.kept < g.n;
+  // R <= 64 without groups: two experts a lane, in registers
+  const bool small = !grouped && R <= 64;
+  uint64_t c0 = 0, c1 = 0;  // this lane's candidates
+
   float top = 0.0f, inv = 0.0f;  // softmax: the largest logit, 1 / sum of the exponentials
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e = j * 32 + lane;
-    key[j] = e < R ? lr[e] : -INFINITY;
+  float l0 = -INFINITY, l1 = -INFINITY, bias0 = 0.0f, bias1 = 0.0f;  // small: this lane's
+  if (small) {
+    if (lane < R) l0 = lr[lane];
+    if (lane + 32 < R) l1 = lr[lane + 32];
+    if (bias != nullptr) {
+      if (lane < R) bias0 = bias[lane];
+      if (lane + 32 < R) bias1 = bias[lane + 32];
+    }
   }
   if (SOFTMAX) {
-    top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) top = fmaxf(top, key[j]);
+    top = fmaxf(l0, l1);
+    if (!small) {
+#pragma unroll 8
+      for (int e = lane; e < R; e += 32) top = fmaxf(top, lr[e]);
+    }
     top = warp_max(top);
     if (top == -INFINITY) top = 0.0f;  // no expert is open: every score is 0
     float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      key[j] = ex2((key[j] - top) * kLog2e);
-      sum += key[j];
+    if (small) {
+      sum = ex2((l0 - top) * kLog2e) + ex2((l1 - top) * kLog2e);
+    } else {
+#pragma unroll 8
+      for (int e = lane; e < R; e += 32) sum += ex2((lr[e] - top) * kLog2e);  // from L1
     }
     sum = warp_sum(sum);
     inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   }
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e = j * 32 + lane;
-    const float s = SOFTMAX ? key[j] * inv : rcp(1.0f + ex2(-kLog2e * key[j]));
-    key[j] = s + (bias != nullptr && e < R ? bias[e] : 0.0f);
-  }
-  uint32_t closed = 0;  // bit j: value j is not to be chosen (VPL > 32: found again below)
-  const uint32_t* bits = nullptr;
-  if (g.kept < g.n) bits = keep_groups<VPL>(g, key, R, sm_keys + warp * g.words());
-  auto is_open = [&](int j) {
-    const int e = j * 32 + lane;
-    if (e >= R) return false;
-    if (bits == nullptr) return true;
-    const int gi = group_of(g, e);
-    return ((bits[gi >> 5] >> (gi & 31)) & 1u) != 0;
+  auto key_of = [&](float l, float b) {
+    return (SOFTMAX ? ex2((l - top) * kLog2e) * inv : rcp(1.0f + ex2(-kLog2e * l))) + b;
   };
-  float lmax = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const bool open = is_open(j);
-    if (VPL <= 32 && !open) closed |= 1u << (j & 31);
-    if (open) lmax = fmaxf(lmax, fmaxf(key[j], -FLT_MAX));
+  auto candidate = [&](float v, int e) { return (uint64_t)key_code(v) << 32 | (uint32_t)~e; };
+  if (small) {
+    const float v0 = key_of(l0, bias0), v1 = key_of(l1, bias1);
+    if (lane < R) c0 = candidate(v0, lane);
+    if (lane + 32 < R) c1 = candidate(v1, lane + 32);
+    if (k > 32) {
+      if (lane < R) key[lane] = v0;
+      if (lane + 32 < R) key[lane + 32] = v1;
+      __syncwarp();
+    }
+  } else {
+#pragma unroll 8
+    for (int e = lane; e < R; e += 32)
+      key[grouped ? e + g.group_of(e) * g.lanes : e] =
+          key_of(lr[e], bias != nullptr ? bias[e] : 0.0f);
+    __syncwarp();
+    if (grouped) keep_groups(g, key, code, list);
   }
-  auto code_of = [&](int j) {
-    return (VPL <= 32 ? (closed >> (j & 31)) & 1u : !is_open(j)) ? 0u : key_code(key[j]);
+
+  // open expert c of `open`: its place among the keys, its number
+  const int open = grouped ? g.kept * g.size : R;
+  auto place = [&](int c) {
+    if (!grouped) return c;
+    const int a = g.group_of(c);
+    return list[a] * (g.size + g.lanes) + c - a * g.size;
+  };
+  auto expert = [&](int c) {
+    if (!grouped) return c;
+    const int a = g.group_of(c);
+    return list[a] * g.size + c - a * g.size;
   };
   int32_t* ids_row = ids + t * k;
   float* probs_row = probs + t * k;
   float sum = 0.0f;
-  auto done = [&](int base, int slots, int chosen) {
+  // slots base ... base + slots - 1 go to the experts that lanes 0 ... hold
+  auto write_slots = [&](int base, int slots, int chosen) {
     float s = 0.0f;
     if (lane < slots) {
       const float l = lr[chosen];
@@ -248,53 +239,79 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
       probs_row[base + lane] = s;
     }
   };
-  int total = 65;
-  if (VPL > 2 && k <= 32) {
-    // keys of -inf and NaN count as the lowest finite ones here: a superset
-    const float least =
-        decode_key(max(1u, __shfl_sync(kAll, warp_sort_desc(key_code(lmax)), k - 1)));
-    int mine = 0;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const bool open = VPL <= 32 ? !((closed >> (j & 31)) & 1u) : is_open(j);
-      mine += open && fmaxf(key[j], -FLT_MAX) >= least ? 1 : 0;
+
+  int total = small ? R : 65;  // candidates
+  if (!small && k <= 32) {
+    float least = -INFINITY;  // keys of -inf and NaN count as the lowest finite ones: a superset
+    if (open > 64) {
+      float lmax = -INFINITY;
+#pragma unroll 4
+      for (int c = lane; c < open; c += 32) lmax = fmaxf(lmax, fmaxf(key[place(c)], -FLT_MAX));
+      least = decode_key(__shfl_sync(kAll, warp_sort_desc(key_code(lmax)), k - 1));
     }
-    int incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(kAll, incl, off);
-      if (lane >= off) incl += o;
+    total = 0;
+#pragma unroll 2
+    for (int base = 0; base < open; base += 32) {
+      const int c = base + lane;
+      const float v = c < open ? key[place(c)] : 0.0f;
+      const bool in = c < open && fmaxf(v, -FLT_MAX) >= least;
+      const uint32_t m = __ballot_sync(kAll, in);
+      if (m == 0) continue;
+      const int at = total + __popc(m & ((1u << lane) - 1u));
+      if (in && at < 64) cand[at] = candidate(v, expert(c));
+      total += __popc(m);
     }
-    total = __shfl_sync(kAll, incl, 31);
-    if (total <= 64) {
-      int at = incl - mine;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const bool open = VPL <= 32 ? !((closed >> (j & 31)) & 1u) : is_open(j);
-        if (open && fmaxf(key[j], -FLT_MAX) >= least)
-          cand[warp][at++] = (uint64_t)key_code(key[j]) << 32 | (uint32_t)~(j * 32 + lane);
+    __syncwarp();
+    if (lane < total) c0 = cand[lane];
+    if (lane + 32 < total) c1 = cand[lane + 32];
+  }
+  if (total <= 64 && k <= 32) {
+    int chosen = 0;
+    if (small || 3 * k < total) {  // k rounds of two reductions, some 14 instructions each
+      for (int slot = 0; slot < k; ++slot) {
+        const uint32_t h0 = (uint32_t)(c0 >> 32), h1 = (uint32_t)(c1 >> 32);
+        const uint32_t m = __reduce_max_sync(kAll, max(h0, h1));
+        const uint32_t l0 = h0 == m ? (uint32_t)c0 : 0u, l1 = h1 == m ? (uint32_t)c1 : 0u;
+        const uint32_t best = __reduce_max_sync(kAll, max(l0, l1));
+        if (h0 == m && (uint32_t)c0 == best) c0 = 0;
+        if (h1 == m && (uint32_t)c1 == best) c1 = 0;
+        if (slot == lane) chosen = (int)~best;
       }
-      __syncwarp();
-      const uint64_t c0 = lane < total ? cand[warp][lane] : 0;
-      const uint64_t c1 = lane + 32 < total ? cand[warp][lane + 32] : 0;
+    } else {  // some 5 instructions a candidate
       int r0 = 0, r1 = 0;
 #pragma unroll 4
       for (int i = 0; i < total; ++i) {
-        const uint64_t c = cand[warp][i];
+        const uint64_t c = cand[i];
         r0 += c > c0;
         r1 += c > c1;
       }
-      if (c0 != 0 && r0 < k) slot_e[warp][r0] = (int)~(uint32_t)c0;
-      if (c1 != 0 && r1 < k) slot_e[warp][r1] = (int)~(uint32_t)c1;
+      if (c0 != 0 && r0 < k) slot_e[r0] = (int)~(uint32_t)c0;
+      if (c1 != 0 && r1 < k) slot_e[r1] = (int)~(uint32_t)c1;
       __syncwarp();
-      done(0, k, lane < k ? slot_e[warp][lane] : 0);
+      if (lane < k) chosen = slot_e[lane];
     }
+    write_slots(0, k, chosen);
+    return;
   }
-  if (total > 64) {
-    uint32_t code[VPL];
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) code[j] = code_of(j);
-    select_rounds<VPL>(code, k, done);
+  for (int base = 0; base < k; base += 32) {
+    const int slots = min(32, k - base);
+    int chosen = 0;
+    for (int slot = 0; slot < slots; ++slot) {
+      uint32_t best = 0, at = 0;
+      for (int c = lane; c < open; c += 32) {  // ascending: a tie keeps the lower one
+        const float v = key[place(c)];
+        const uint32_t u = __float_as_uint(v) == kTaken ? 0u : key_code(v);
+        if (u > best) {
+          best = u;
+          at = c;
+        }
+      }
+      const uint32_t m = __reduce_max_sync(kAll, best);
+      const int c = (int)__reduce_min_sync(kAll, best == m ? at : 0x7fffffffu);
+      if (lane == (c & 31)) key[place(c)] = __uint_as_float(kTaken);
+      if (slot == lane) chosen = expert(c);
+    }
+    write_slots(base, slots, chosen);
   }
   if (k > 32)  // each lane's own values
     for (int slot = lane; slot < k; slot += 32)
@@ -394,18 +411,18 @@ int values_per_lane(int R) {
     LMOE_VPL(16, CALL) LMOE_VPL(32, CALL) LMOE_VPL(64, CALL) LMOE_VPL(128, CALL) \
   }
 
-template <int VPL, bool SOFTMAX>
+template <bool SOFTMAX>
 static cudaError_t launch_rule(const RouteRule& rule, const Groups& g, const float* logits,
                                int64_t ld, const float* bias, int64_t n, int R, int k, int32_t* ids,
                                float* probs, cudaStream_t st) {
-  const size_t smem = g.kept < g.n ? (size_t)kWarps * g.words() * 4 : 0;
-  if (smem > 40 * 1024) {  // with the candidates' 2 KB, more than a kernel gets unasked
-    cudaError_t e = cudaFuncSetAttribute(route_rule_kernel<VPL, SOFTMAX>,
+  const size_t smem = (size_t)kWarps * g.words() * 4;
+  if (smem > 40 * 1024) {  // with the candidates' 3 KB, more than a kernel gets unasked
+    cudaError_t e = cudaFuncSetAttribute(route_rule_kernel<SOFTMAX>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   count_launch();
-  return launch_pdl(route_rule_kernel<VPL, SOFTMAX>, dim3((unsigned)((n + kWarps - 1) / kWarps)),
+  return launch_pdl(route_rule_kernel<SOFTMAX>, dim3((unsigned)((n + kWarps - 1) / kWarps)),
                     dim3(32 * kWarps), smem, st, 1, logits, ld, bias, n, R, k, g, rule.renormalise,
                     rule.scale, ids, probs);
 }
@@ -417,16 +434,14 @@ cudaError_t launch_route_rule(const RouteRule& rule, const float* logits, int64_
   Groups g;
   g.n = rule.n_groups;
   g.kept = rule.topk_groups;
-  g.size = R / rule.n_groups;
+  if (g.kept == g.n) g.n = g.kept = 1;  // every group is kept: as one
+  g.size = R / g.n;
   g.lanes = 1;
   while (g.lanes * 2 * g.n <= 32) g.lanes *= 2;
   g.top2 = rule.top2;
   g.magic = g.size == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + g.size - 1) / g.size);
-  LMOE_VPL_SWITCH(R, (rule.softmax ? launch_rule<kV, true>(rule, g, logits, ld, bias, n, R, k, ids,
-                                                           probs, st)
-                                   : launch_rule<kV, false>(rule, g, logits, ld, bias, n, R, k, ids,
-                                                            probs, st)))
-  return cudaErrorInvalidValue;
+  return rule.softmax ? launch_rule<true>(rule, g, logits, ld, bias, n, R, k, ids, probs, st)
+                      : launch_rule<false>(rule, g, logits, ld, bias, n, R, k, ids, probs, st);
 }
 
 cudaError_t launch_route_rule_backward(const RouteRule& rule, const float* logits, int64_t ld,
