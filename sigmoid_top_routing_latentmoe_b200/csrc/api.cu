@@ -318,19 +318,26 @@ static lmoe_status run_route_grouped(const lmoe_dims* d, const RouteRule& rule, 
 }
 
 // ------------------------------------------------------- 8-bit routed experts
-// Tiles of the 8-bit products: CTA pairs over 256 rows once experts have 64 rows
-// on average, else single CTAs over 128 (LMOE_FP8_PAIRS=0 or 1 overrides it).
-static bool fp8_pairs(const lmoe_dims* d) {
+// Tiles of an 8-bit product: CTA pairs over 256 rows when experts have more than
+// 128 rows on average, K is at least 512 long and the tiles fill the pairs once;
+// else single CTAs over 128 rows.  Measured (FFN, single / pairs): mid layer with
+// 2048 rows an expert 478 / 440 us, with 128 rows 71.7 / 75.8; K3 width with 146
+// rows 961 / 898 us, with 37 rows 872 / 1182; 0.5b layer (l = 384) with 512 rows
+// 36.9 / 43.0.  LMOE_FP8_PAIRS=0 or 1 overrides it.
+static bool fp8_pairs(const lmoe_dims* d, int n_in, int n_out) {
   if (const char* v = getenv("LMOE_FP8_PAIRS")) {
     if (v[0] == '0') return false;
     if (v[0] == '1') return true;
   }
-  return d->n_tokens * (int64_t)d->top_k >= 64 * (int64_t)d->n_routed;
+  const int64_t rows = d->n_tokens * (int64_t)d->top_k;
+  return rows > 128 * (int64_t)d->n_routed && n_in >= 512 &&
+         (rows + 255) / 256 * ((n_out + 255) / 256) >= 74;
 }
 
-static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* offsets, void* ws) {
+static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* offsets, void* ws,
+                          bool pairs) {
   TileList t;
-  t.tile_m = fp8_pairs(d) ? kRoutedPairTileM : kTileM;
+  t.tile_m = pairs ? kRoutedPairTileM : kTileM;
   t.offsets = offsets; t.R = d->n_routed; t.rows = d->n_tokens * d->top_k;
   t.max_tiles = L.max_tiles;
   t.n_mtiles = &at<WsHeader>(ws, L.header)->n_mtiles;
@@ -362,17 +369,16 @@ static lmoe_status run_expert_ffn_fp8(const lmoe_dims* d, const void* z, const i
   uint8_t* zs = zq + P * Lt;
   uint8_t* hq = at<uint8_t>(ws, L.h);
   uint8_t* hs = hq + P * F;
-  const TileList tl = tile_list(d, L, offsets, ws);
-  const bool pairs = tl.tile_m == kRoutedPairTileM;
+  const bool pairs = fp8_pairs(d, std::min(Lt, F), Lt);  // both products share a tile list
+  const TileList tl = tile_list(d, L, offsets, ws, pairs);
   int32_t* status = &at<WsHeader>(ws, L.header)->status;
   {
     ProfScope ps("quantize", st);
-    LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");
     const bool sorts = fp8_sorts(d);
     uint8_t* tq = sorts ? at<uint8_t>(ws, L.eo) : zq;
     uint8_t* ts = sorts ? tq + d->n_tokens * Lt : zs;
     LMOE_CUDA(launch_quantize_rows<T>((const T*)z, d->n_tokens, Lt, sorts ? nullptr : perm,
-                                      sorts ? d->n_tokens : P, Lt, tq, ts, st),
+                                      sorts ? d->n_tokens : P, Lt, tq, ts, st, &tl),
               "quantize rows");
     if (sorts)
       LMOE_CUDA(launch_sort_rows(tq, ts, d->n_tokens, perm, P, Lt, zq, zs, st), "sort rows");
@@ -1113,12 +1119,13 @@ lmoe_status moe_expert_gemm_fp8(const lmoe_dims* dims, int32_t n_in, int32_t n_o
   ProfJoin pj(st);  // joins the profiling branch on return
   if (dims->n_tokens == 0) return LMOE_OK;
   const Layout L = layout(dims, false);
-  const TileList tl = tile_list(dims, L, offsets, ws);
+  const bool pairs = fp8_pairs(dims, n_in, n_out);
+  const TileList tl = tile_list(dims, L, offsets, ws, pairs);
   Fp8Gemm g{};
   g.a = (const uint8_t*)a; g.a_scales = a_scales; g.rows = tl.rows; g.R = dims->n_routed;
   g.n_in = n_in; g.n_out = n_out; g.w = (const uint8_t*)w; g.w_scales = w_scales; g.out = out;
   g.out_f32 = dims->dtype == LMOE_F32 ? 1 : 0;
-  g.pairs = tl.tile_m == kRoutedPairTileM;
+  g.pairs = pairs;
   if (offsets != nullptr) {
     g.tiles = tl.tiles; g.n_mtiles = tl.n_mtiles; g.max_tiles = tl.max_tiles;
     LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");

@@ -13,7 +13,8 @@ constexpr int kQBlock = 128;
 inline int q_words(int64_t cols) { return (int)((cols + 511) / 512); }
 inline int q_blocks(int64_t n) { return (int)((n + kQBlock - 1) / kQBlock); }
 
-// Tile list of a ragged product (launch_expert_tiles): (expert, first row, rows) of at most
+// Tile list of a ragged product, written by launch_expert_tiles or by a block of
+// the quantiser of its rows: (expert, first row, rows) of at most
 // tile_m rows.
 struct TileList {
   const int32_t* offsets;  // [R + 1], clamped to [0, rows]
@@ -32,7 +33,7 @@ struct TileList {
 template <typename T>
 cudaError_t launch_quantize_rows(const T* x, int64_t n_src, int64_t ld, const int32_t* index,
                                  int64_t rows, int cols, uint8_t* q, uint8_t* scales,
-                                 cudaStream_t st);
+                                 cudaStream_t st, const TileList* tiles = nullptr);
 // Quantised rows in another order: row r is row index[r], zeros outside [0, n_src).
 cudaError_t launch_sort_rows(const uint8_t* q, const uint8_t* scales, int64_t n_src,
                              const int32_t* index, int64_t rows, int cols, uint8_t* q_out,

@@ -87,11 +87,60 @@ __device__ __forceinline__ float lanes_max(float m) {
   return m;
 }
 
+// The tile list of a ragged product: expert e's rows [offsets[e], offsets[e + 1])
+// in tiles of at most tile_m.  Offsets are clamped to an ascending order inside
+// [0, rows] and the list to max_tiles, so that no list leads a product out of
+// its buffers.  One block of kTileThreads; a block-wide scan over as many experts
+// at a time.
+constexpr int kTileThreads = 256;
+__device__ __forceinline__ void build_tile_list(const TileList& t) {
+  __shared__ int warp_sum[kTileThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int base = 0;
+  for (int e0 = 0; e0 < t.R; e0 += kTileThreads) {
+    const int e = e0 + threadIdx.x;
+    int lo = 0, hi = 0;
+    if (e < t.R) {
+      lo = (int)min((int64_t)max(t.offsets[e], 0), t.rows);
+      hi = (int)min((int64_t)max(t.offsets[e + 1], lo), t.rows);
+    }
+    const int n = (hi - lo + t.tile_m - 1) / t.tile_m;
+    int inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kTileThreads / 32; ++w) {
+      const int s = warp_sum[w];
+      if (w < warp) before += s;
+      total += s;
+    }
+    int at = base + before + inc - n;
+    for (int j = 0; j < n; ++j, ++at)
+      if (at < t.max_tiles)
+        t.tiles[at] = make_int4(e, lo + j * t.tile_m, min(t.tile_m, hi - lo - j * t.tile_m), 0);
+    base += total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *t.n_mtiles = min(base, t.max_tiles);
+}
+__global__ void __launch_bounds__(kTileThreads) expert_tiles_kernel(TileList t) {
+  pdl_trigger();
+  pdl_wait();
+  build_tile_list(t);
+}
+
 // One warp per row, 512 columns a step: a lane holds 16 neighbouring elements,
 // eight lanes a block, and the step's four exponents are one word of scales.
 // The kernel is bound by issue slots rather than bytes (with 8 elements a lane,
 // 140 instructions for every 8, the mid layer's 131072 rows of 1024 took 72 us),
-// so 16 elements share the reductions and addresses.
+// so 16 elements share the reductions and addresses.  One more block writes the
+// tile list of the products that follow, when there is one.
 constexpr int kLaneElems = 16, kStepCols = 32 * kLaneElems, kRowWarps = 8;
 template <typename T>
 struct LaneElems {
@@ -132,9 +181,13 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kRowWarps)
     quantize_rows_kernel(const T* __restrict__ x, int64_t n_src, int64_t ld,
                          const int32_t* __restrict__ index, int64_t rows, int cols,
-                         uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+                         uint8_t* __restrict__ q, uint8_t* __restrict__ scales, TileList tiles) {
   pdl_trigger();
   pdl_wait();
+  if (tiles.tiles != nullptr && blockIdx.x == gridDim.x - 1) {  // a block of its own
+    if (blockIdx.y == 0) build_tile_list(tiles);
+    return;
+  }
   constexpr int U = 2;  // steps whose loads are in flight together
   const int lane = threadIdx.x & 31;
   const int64_t r = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
@@ -259,68 +312,29 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   }
 }
 
-// The tile list of a ragged product: expert e's rows [offsets[e], offsets[e + 1])
-// in tiles of at most tile_m.  Offsets are clamped to an ascending order inside
-// [0, rows] and the list to max_tiles, so that no list leads a product out of
-// its buffers.  One block; a block-wide scan over 1024 experts at a time.
-__global__ void __launch_bounds__(1024) expert_tiles_kernel(TileList t) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ int warp_sum[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int base = 0;
-  for (int e0 = 0; e0 < t.R; e0 += 1024) {
-    const int e = e0 + threadIdx.x;
-    int lo = 0, hi = 0;
-    if (e < t.R) {
-      lo = (int)min((int64_t)max(t.offsets[e], 0), t.rows);
-      hi = (int)min((int64_t)max(t.offsets[e + 1], lo), t.rows);
-    }
-    const int n = (hi - lo + t.tile_m - 1) / t.tile_m;
-    int inc = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < 32; ++w) {
-      const int s = warp_sum[w];
-      if (w < warp) before += s;
-      total += s;
-    }
-    int at = base + before + inc - n;
-    for (int j = 0; j < n; ++j, ++at)
-      if (at < t.max_tiles)
-        t.tiles[at] = make_int4(e, lo + j * t.tile_m, min(t.tile_m, hi - lo - j * t.tile_m), 0);
-    base += total;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) *t.n_mtiles = min(base, t.max_tiles);
-}
-
 }  // namespace
 
 template <typename T>
 cudaError_t launch_quantize_rows(const T* x, int64_t n_src, int64_t ld, const int32_t* index,
                                  int64_t rows, int cols, uint8_t* q, uint8_t* scales,
-                                 cudaStream_t st) {
+                                 cudaStream_t st, const TileList* tiles) {
+  static_assert(kTileThreads == 32 * kRowWarps, "one block writes the tile list");
   if (rows == 0) return cudaSuccess;
   const unsigned blocks = (unsigned)((rows + kRowWarps - 1) / kRowWarps);
   // few rows: their steps are spread over up to 8 warps each, towards 1200 blocks
   const int pairs = (cols + 2 * kStepCols - 1) / (2 * kStepCols);
   const unsigned split = std::min<unsigned>(std::min(pairs, 8), std::max(1u, 1200 / blocks));
   count_launch();
-  return launch_pdl(quantize_rows_kernel<T>, dim3(blocks, split), dim3(32 * kRowWarps), 0, st, 1, x,
-                    n_src, ld, index, rows, cols, q, scales);
+  return launch_pdl(quantize_rows_kernel<T>, dim3(blocks + (tiles != nullptr ? 1 : 0), split),
+                    dim3(32 * kRowWarps), 0, st, 1, x, n_src, ld, index, rows, cols, q, scales,
+                    tiles != nullptr ? *tiles : TileList{});
 }
 template cudaError_t launch_quantize_rows<float>(const float*, int64_t, int64_t, const int32_t*,
-                                                 int64_t, int, uint8_t*, uint8_t*, cudaStream_t);
+                                                 int64_t, int, uint8_t*, uint8_t*, cudaStream_t,
+                                                 const TileList*);
 template cudaError_t launch_quantize_rows<__nv_bfloat16>(const __nv_bfloat16*, int64_t, int64_t,
                                                          const int32_t*, int64_t, int, uint8_t*,
-                                                         uint8_t*, cudaStream_t);
+                                                         uint8_t*, cudaStream_t, const TileList*);
 
 cudaError_t launch_sort_rows(const uint8_t* q, const uint8_t* scales, int64_t n_src,
                              const int32_t* index, int64_t rows, int cols, uint8_t* q_out,
@@ -349,7 +363,7 @@ template cudaError_t launch_quantize_weights<__nv_bfloat16>(const __nv_bfloat16*
 
 cudaError_t launch_expert_tiles(const TileList& t, cudaStream_t st) {
   count_launch();
-  return launch_pdl(expert_tiles_kernel, dim3(1), dim3(1024), 0, st, 1, t);
+  return launch_pdl(expert_tiles_kernel, dim3(1), dim3(kTileThreads), 0, st, 1, t);
 }
 
 }  // namespace lmoe
