@@ -26,65 +26,60 @@ namespace {
 template <typename T>
 constexpr int kVec = 16 / sizeof(T);  // elements of a 16-byte vector
 
+// Element i of a vector.
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[kVec<T>]);
-template <>
-__device__ __forceinline__ void unpack<float>(const uint4& v, float (&f)[4]) {
-  f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
-  f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
-}
-template <>
-__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ float elem(const uint4& v, int i) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  if constexpr (kVec<T> == 4) return __uint_as_float(w[i]);
+  else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
 }
-// Largest magnitude of a vector, NaN left out; FINITE leaves infinities out too
-// (the kernels take that way only for a block whose first answer is infinite).
-template <typename T, bool FINITE>
-__device__ __forceinline__ float vec_amax(const uint4& v) {
-  if constexpr (kVec<T> == 8 && !FINITE) {  // bf16 pairs: 8 instructions
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])),
-                                     __hmax2(__habs2(h[2]), __habs2(h[3])));
-    return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.0f);  // 0 where all are NaN
-  } else {
-    float f[kVec<T>];
-    unpack<T>(v, f);
-    float m = 0.0f;
+// Magnitudes in order as whole numbers: the bits of |x|, which go from 0 to
+// kInfBits for finite and infinite values and beyond for NaN.
+constexpr uint32_t kInfBits = 0x7f800000u;
+// The largest of a lane's N vectors (bf16: two elements at a time).
+template <typename T, int N>
+__device__ __forceinline__ uint32_t amax_bits(const uint4 (&v)[N]) {
+  constexpr uint32_t kAbs = kVec<T> == 4 ? 0x7fffffffu : 0x7fff7fffu;
+  uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kVec<T>; ++i) m = FINITE ? finite_max(m, f[i]) : fmaxf(m, fabsf(f[i]));
-    return m;
+  for (int i = 0; i < N; ++i) {
+    if constexpr (kVec<T> == 4) {
+      m = __vimax3_u32(m, v[i].x & kAbs, v[i].y & kAbs);
+      m = __vimax3_u32(m, v[i].z & kAbs, v[i].w & kAbs);
+    } else {
+      m = __vimax3_u16x2(m, v[i].x & kAbs, v[i].y & kAbs);
+      m = __vimax3_u16x2(m, v[i].z & kAbs, v[i].w & kAbs);
+    }
   }
+  return kVec<T> == 4 ? m : max(m & 0xffffu, m >> 16) << 16;
 }
-// Quantises the vector's elements, four to a word.
-template <typename T, bool FINITE>
-__device__ __forceinline__ void quantize_vec(const uint4& v, float inv, uint32_t* w) {
-  float f[kVec<T>];
-  unpack<T>(v, f);
+// The same over finite elements only, for a block that holds others.
+template <typename T, int N>
+__device__ __forceinline__ uint32_t finite_amax_bits(const uint4 (&v)[N]) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kVec<T> / 4; ++i) {
-    const float a = f[4 * i] * inv, b = f[4 * i + 1] * inv, c = f[4 * i + 2] * inv,
-                d = f[4 * i + 3] * inv;
-    w[i] = FINITE ? pack_e4m3(a, b, c, d) : pack_e4m3_finite(a, b, c, d);
-  }
-}
-template <typename T, bool FINITE>
-__device__ __forceinline__ void store_q(uint8_t* q, const uint4& v, float inv) {
-  uint32_t w[kVec<T> / 4];
-  quantize_vec<T, FINITE>(v, inv, w);
-  if constexpr (kVec<T> == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t*>(q) = w[0];
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec<T>; ++j) m = finite_max(m, elem<T>(v[i], j));
+  return __float_as_uint(m);
 }
 template <int LANES>
-__device__ __forceinline__ float lanes_max(float m) {
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
 #pragma unroll
   for (int off = LANES / 2; off > 0; off >>= 1)
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
   return m;
+}
+// A vector's elements times inv, rounded, four to a word.  FINITE: none is
+// infinite.
+template <typename T, bool FINITE>
+__device__ __forceinline__ void quantize_vec(const uint4& v, float inv, uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < kVec<T> / 4; ++i) {
+    const float a = elem<T>(v, 4 * i) * inv, b = elem<T>(v, 4 * i + 1) * inv,
+                c = elem<T>(v, 4 * i + 2) * inv, d = elem<T>(v, 4 * i + 3) * inv;
+    w[i] = FINITE ? pack_e4m3_finite(a, b, c, d) : pack_e4m3(a, b, c, d);
+  }
 }
 
 // The tile list of a ragged product: expert e's rows [offsets[e], offsets[e + 1])
@@ -142,39 +137,12 @@ __global__ void __launch_bounds__(kTileThreads) expert_tiles_kernel(TileList t) 
 // so 16 elements share the reductions and addresses.  One more block writes the
 // tile list of the products that follow, when there is one.
 constexpr int kLaneElems = 16, kStepCols = 32 * kLaneElems, kRowWarps = 8;
-template <typename T>
-struct LaneElems {
-  uint4 v[kLaneElems / kVec<T>];
-};
-template <typename T>
-__device__ __forceinline__ LaneElems<T> load_elems(const T* x, bool have) {
-  LaneElems<T> e;
-#pragma unroll
-  for (int i = 0; i < kLaneElems / kVec<T>; ++i)
-    e.v[i] = have ? reinterpret_cast<const uint4*>(x)[i] : make_uint4(0, 0, 0, 0);
-  return e;
-}
 template <typename T, bool FINITE>
-__device__ __forceinline__ float lane_amax(const LaneElems<T>& e) {
-  if constexpr (kVec<T> == 8 && !FINITE) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(e.v);
-    __nv_bfloat162 m = __habs2(h[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(h[i]));
-    return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.0f);
-  } else {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kLaneElems / kVec<T>; ++i) m = fmaxf(m, vec_amax<T, FINITE>(e.v[i]));
-    return m;
-  }
-}
-template <typename T, bool FINITE>
-__device__ __forceinline__ uint4 lane_q(const LaneElems<T>& e, float inv) {
+__device__ __forceinline__ uint4 lane_q(const uint4 (&v)[kLaneElems / kVec<T>], float inv) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < kLaneElems / kVec<T>; ++i)
-    quantize_vec<T, FINITE>(e.v[i], inv, w + i * kVec<T> / 4);
+    quantize_vec<T, FINITE>(v[i], inv, w + i * kVec<T> / 4);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <typename T>
@@ -204,26 +172,28 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   uint8_t* sr = scales + r * 4 + (lane >> 3);
   // a long row of few rows is shared by gridDim.y warps
   for (int s0 = blockIdx.y * U; s0 < steps; s0 += gridDim.y * U) {
-    LaneElems<T> e[U];
+    constexpr int NV = kLaneElems / kVec<T>;
+    uint4 v[U][NV];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      e[u] = load_elems(xr + (s0 + u) * kStepCols,
-                        have && (s0 + u) * kStepCols + lane * kLaneElems < cols);
+    for (int u = 0; u < U; ++u) {
+      const bool in = have && (s0 + u) * kStepCols + lane * kLaneElems < cols;
+      const uint4* at = reinterpret_cast<const uint4*>(xr + (s0 + u) * kStepCols);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[u][j] = in ? at[j] : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int step = s0 + u;
       if (step >= steps) break;
-      const bool in = step * kStepCols + lane * kLaneElems < cols;
-      float m = lanes_max<8>(lane_amax<T, false>(e[u]));
-      uint4 w;
-      if (__any_sync(0xffffffffu, m == INFINITY)) {
-        m = lanes_max<8>(lane_amax<T, true>(e[u]));
-        w = lane_q<T, true>(e[u], pow2_f(-scale_exponent(m)));
-      } else {
-        w = lane_q<T, false>(e[u], pow2_f(-scale_exponent(m)));
-      }
-      if (in) *reinterpret_cast<uint4*>(qr + step * kStepCols) = w;
-      if ((lane & 7) == 0) sr[(int64_t)step * rows * 4] = (uint8_t)(scale_exponent(m) + 127);
+      uint32_t m = lanes_max<8>(amax_bits<T>(v[u]));
+      const bool finite = !__any_sync(0xffffffffu, m >= kInfBits);
+      if (!finite) m = lanes_max<8>(finite_amax_bits<T>(v[u]));
+      const int e = scale_exponent(__uint_as_float(m));
+      const float inv = pow2_f(-e);
+      const uint4 w = finite ? lane_q<T, true>(v[u], inv) : lane_q<T, false>(v[u], inv);
+      if (step * kStepCols + lane * kLaneElems < cols)
+        *reinterpret_cast<uint4*>(qr + step * kStepCols) = w;
+      if ((lane & 7) == 0) sr[(int64_t)step * rows * 4] = (uint8_t)(e + 127);
     }
   }
 }
@@ -237,7 +207,7 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const T* __restri
   pdl_trigger();
   pdl_wait();
   constexpr int V = kVec<T>, BL = kQBlock / V, RP = 256 / BL, U = kQBlock / RP;
-  __shared__ float part[8];
+  __shared__ uint32_t part[8];
   const int64_t blk = blockIdx.x;
   const int cbi = (int)(blk % cb4);
   const int rbi = (int)((blk / cb4) % rb);
@@ -252,32 +222,31 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const T* __restri
     if (c < cols && r < rows)
       v[u] = *reinterpret_cast<const uint4*>(w + (mat * rows + r) * cols + c);
   }
-  float m = 0.0f;
-#pragma unroll
-  for (int u = 0; u < U; ++u) m = fmaxf(m, vec_amax<T, false>(v[u]));
-  bool finite = true;  // of the block's maximum
-  for (int pass = 0; pass < 2; ++pass) {
+  uint32_t m = amax_bits<T>(v);
+  bool finite = true;  // every element of the block
+  for (;;) {
     m = lanes_max<32>(m);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
-    if (m < INFINITY) break;
+    for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+    if (m < kInfBits) break;
     finite = false;
-    m = 0.0f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) m = fmaxf(m, vec_amax<T, true>(v[u]));
+    m = finite_amax_bits<T>(v);
     __syncthreads();
   }
-  const int e = scale_exponent(m);
+  const int e = scale_exponent(__uint_as_float(m));
   const float inv = pow2_f(-e);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t r = r0 + u * RP;
     if (c < cols && r < rows) {
+      uint32_t o[V / 4];
+      if (finite) quantize_vec<T, true>(v[u], inv, o);
+      else quantize_vec<T, false>(v[u], inv, o);
       uint8_t* dst = q + (mat * rows + r) * cols + c;
-      if (finite) store_q<T, false>(dst, v[u], inv);
-      else store_q<T, true>(dst, v[u], inv);
+      if constexpr (V == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = o[0];
     }
   }
   if (threadIdx.x == 0) scales[blk] = (uint8_t)(e + 127);
