@@ -19,6 +19,12 @@ F8 = torch.float8_e4m3fn
 ROUND = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 
 
+@pytest.fixture(params=["0", "1"], ids=["single", "pairs"])
+def tiles(request, monkeypatch):
+    """Single CTAs over 128-row tiles, CTA pairs over 256-row ones."""
+    monkeypatch.setenv("LMOE_FP8_PAIRS", request.param)
+
+
 def gpu(a, dtype=None):
     t = torch.from_numpy(np.ascontiguousarray(a))
     return (t if dtype is None else t.to(dtype)).cuda()
@@ -150,7 +156,7 @@ def check_gemm(got, av, wv, offsets, dtype, fill=7.0):
     (129, 2, 1, 2064, 520),
     (640, 300, 2, 256, 256),     # more experts than some of them have rows
 ])
-def test_expert_gemm(n, R, k, n_in, n_out, dtype):
+def test_expert_gemm(tiles, n, R, k, n_in, n_out, dtype):
     rng = np.random.default_rng(n + n_in)
     av, a, a_s = quantized_rows(rng, n * k, n_in)
     wv, w, w_s = quantized_weights(rng, R, n_out, n_in)
@@ -159,8 +165,8 @@ def test_expert_gemm(n, R, k, n_in, n_out, dtype):
     check_gemm(got, av, wv, offsets, dtype)
 
 
-@pytest.mark.parametrize("rows", [1, 31, 32, 33, 127, 128, 129, 1000])
-def test_expert_gemm_dense(rows):
+@pytest.mark.parametrize("rows", [1, 31, 32, 33, 127, 128, 129, 256, 257, 1000])
+def test_expert_gemm_dense(tiles, rows):
     rng = np.random.default_rng(rows)
     av, a, a_s = quantized_rows(rng, rows, 400)
     wv, w, w_s = quantized_weights(rng, 1, 392, 400)
@@ -170,7 +176,7 @@ def test_expert_gemm_dense(rows):
     np.testing.assert_array_equal(got, run_gemm(d, a, a_s, np.array([0, rows], np.int32), w, w_s, 392))
 
 
-def test_expert_gemm_rows_of_no_expert():
+def test_expert_gemm_rows_of_no_expert(tiles):
     rng = np.random.default_rng(5)
     av, a, a_s = quantized_rows(rng, 400, 256)
     wv, w, w_s = quantized_weights(rng, 3, 256, 256)
@@ -179,7 +185,7 @@ def test_expert_gemm_rows_of_no_expert():
     check_gemm(got, av, wv, offsets, torch.bfloat16)
 
 
-def test_expert_gemm_bad_offsets_stay_inside():
+def test_expert_gemm_bad_offsets_stay_inside(tiles):
     """Offsets outside the rows or out of order are clamped: no row out of range is touched."""
     rng = np.random.default_rng(6)
     av, a, a_s = quantized_rows(rng, 300, 128)
@@ -192,7 +198,7 @@ def test_expert_gemm_bad_offsets_stay_inside():
     assert (np.abs(got - want) <= tol)[sure].all()
 
 
-def test_expert_gemm_scales_over_the_range():
+def test_expert_gemm_scales_over_the_range(tiles):
     """Row and weight scales far from 1, each block with its own."""
     rng = np.random.default_rng(8)
     x = rng.standard_normal((150, 640)) * np.repeat(2.0 ** rng.integers(-60, 60, (150, 5)), 128, 1)
@@ -205,7 +211,7 @@ def test_expert_gemm_scales_over_the_range():
     check_gemm(got, av, wv, offsets, torch.float32)
 
 
-def test_expert_gemm_nan_stays_in_its_row():
+def test_expert_gemm_nan_stays_in_its_row(tiles):
     rng = np.random.default_rng(9)
     x = rng.standard_normal((140, 256))
     x[130, 5] = np.nan
@@ -217,7 +223,7 @@ def test_expert_gemm_nan_stays_in_its_row():
     check_gemm(got[ok], av[ok], wv, [0, 139], torch.bfloat16)
 
 
-def test_expert_gemm_input_gradient():
+def test_expert_gemm_input_gradient(tiles):
     """dA = dOut W: the same product with the transposed weights and scales."""
     rng = np.random.default_rng(10)
     R, n_out, n_in, P = 3, 272, 400, 260
@@ -274,7 +280,7 @@ def check_ffn(got, z, perm, offsets, weights, dtype, b1=4.0, b2=25.0, fill=7.0):
     (64, 100, 4, 272, 1040, torch.float32),
     (500, 2, 2, 640, 528, torch.bfloat16),
 ])
-def test_expert_ffn(n, R, k, latent, ff, dtype):
+def test_expert_ffn(tiles, n, R, k, latent, ff, dtype):
     rng = np.random.default_rng(n + latent)
     z, perm, offsets, weights = ffn_case(rng, n, R, k, latent, ff, dtype)
     d = dims_of(n, R, k, latent, ff, dtype)
@@ -283,7 +289,7 @@ def test_expert_ffn(n, R, k, latent, ff, dtype):
     check_ffn(out.double().cpu().numpy(), z, perm, offsets, weights, dtype)
 
 
-def test_expert_ffn_wide_activations():
+def test_expert_ffn_wide_activations(tiles):
     """Pre-activations over +-15: the saturated ends of the gate, other caps than the defaults."""
     rng = np.random.default_rng(3)
     z, perm, offsets, weights = ffn_case(rng, 60, 4, 2, 256, 256, torch.bfloat16, w_std=0.4)
@@ -292,7 +298,7 @@ def test_expert_ffn_wide_activations():
     check_ffn(out.double().cpu().numpy(), z, perm, offsets, weights, torch.bfloat16, 2.0, 7.0)
 
 
-def test_expert_ffn_dropped_rows_and_stray_tokens():
+def test_expert_ffn_dropped_rows_and_stray_tokens(tiles):
     """Sorted slots behind the last expert keep what they held; perm entries there are not read as rows."""
     rng = np.random.default_rng(4)
     z, perm, offsets, weights = ffn_case(rng, 100, 3, 2, 128, 256, torch.bfloat16)
@@ -303,7 +309,7 @@ def test_expert_ffn_dropped_rows_and_stray_tokens():
     check_ffn(out.double().cpu().numpy(), z, perm, offsets, weights, torch.bfloat16)
 
 
-def test_expert_ffn_repeats_streams_and_graphs():
+def test_expert_ffn_repeats_streams_and_graphs(tiles):
     """The same bits on every call, on another stream and from a replayed graph with new inputs."""
     rng = np.random.default_rng(11)
     z, perm, offsets, weights = ffn_case(rng, 200, 6, 2, 384, 272, torch.bfloat16)
@@ -331,6 +337,110 @@ def test_expert_ffn_repeats_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     check_ffn(out.double().cpu().numpy(), z2, perm, off2, weights, torch.bfloat16)
+
+
+@pytest.mark.parametrize("n,R,k,latent,ff", [(3000, 5, 4, 1536, 512), (2500, 9, 8, 1024, 528)])
+def test_expert_ffn_many_rows(n, R, k, latent, ff):
+    """Enough to quantise once per token and sort, and for the tile rule to take pairs; a sample of
+    the rows is compared."""
+    rng = np.random.default_rng(n)
+    z = torch.from_numpy(rng.standard_normal((n, latent))).to(torch.bfloat16)
+    offsets = offsets_of(rng, n * k, R, 0.5)
+    offsets[-1] -= 7                                    # dropped rows at the end
+    perm = rng.integers(0, n, n * k).astype(np.int32)
+    perm[-7:] = -1
+    weights = [quantized_weights(rng, R, r, c, 0.05) for r, c in ((ff, latent), (ff, latent), (latent, ff))]
+    out, ws = run_ffn(dims_of(n, R, k, latent, ff), z.cuda(), gpu(perm), gpu(offsets), weights)
+    assert lm.get_device_status(ws) == lm.OK
+    got = out.double().cpu().numpy()
+    assert (got[-7:] == 7.0).all()
+    for e in range(R):
+        lo, hi = offsets[e], offsets[e + 1]
+        if hi == lo:
+            continue
+        rows = np.unique(np.r_[lo, (lo + hi) // 2, hi - 1, rng.integers(lo, hi, 6)])
+        want, bound = ref.ffn(z.double().numpy(), perm[rows], [0, len(rows)], *[v[e:e + 1] for v, _, _ in weights],
+                              4.0, 25.0)
+        assert (np.abs(got[rows] - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound)).all(), e
+
+
+def test_offsets_past_32_bits():
+    """Rows whose byte and element offsets pass 2^31 and 2^32."""
+    rng = np.random.default_rng(2)
+    n, cols = 290_000, 16384                            # 4.75e9 quantised bytes
+    x = torch.from_numpy(rng.standard_normal((64, cols))).to(torch.bfloat16).cuda()
+    index = torch.arange(n, dtype=torch.int32, device="cuda") % 64
+    q = torch.empty(n, cols, dtype=F8, device="cuda")
+    s = torch.empty(lm.fp8_row_scales_shape(n, cols), dtype=torch.uint8, device="cuda")
+    lm.quantize_rows_fp8(x, q, s, index=index)
+    want = torch.empty(64, cols, dtype=F8, device="cuda"), torch.empty(cols // 512, 64, 4, dtype=torch.uint8, device="cuda")
+    lm.quantize_rows_fp8(x, *want)
+    tail = slice(n - 64, n)
+    order = index[tail].long()
+    assert torch.equal(q[tail].view(torch.uint8), want[0].view(torch.uint8)[order])
+    assert torch.equal(s[:, tail], want[1][:, order])
+    # a product that reads them, and one that writes past 2^32 bytes
+    wv, w, w_s = quantized_weights(rng, 1, 8, cols)
+    d = dims_of(n, 1, 1)
+    ws = lm.alloc_workspace(d)
+    out = torch.empty(n, 8, dtype=torch.bfloat16, device="cuda")
+    lm.moe_expert_gemm_fp8(d, q, s, None, w, w_s, out, ws)
+    av = ref.quantize_blocks(x.double().cpu().numpy(), 1, 128)[2][order.cpu().numpy()]
+    check_gemm(out[tail].double().cpu().numpy(), av, wv, [0, 64], torch.bfloat16)
+    del q, s, out
+    av, a, a_s = quantized_rows(rng, 64, 16)
+    rows = index[:150_000].long()
+    wv, w, w_s = quantized_weights(rng, 1, cols, 16)
+    d = dims_of(150_000, 1, 1)
+    big = torch.empty(150_000, cols, dtype=torch.bfloat16, device="cuda")
+    lm.moe_expert_gemm_fp8(d, a.view(torch.uint8)[rows].view(F8), a_s[:, rows].contiguous(), None, w, w_s, big,
+                           lm.alloc_workspace(d))
+    check_gemm(big[-64:].double().cpu().numpy(), av[rows[-64:].cpu().numpy()], wv, [0, 64], torch.bfloat16)
+
+
+def test_two_streams_at_once():
+    """Calls that run side by side, each with its own workspace."""
+    rng = np.random.default_rng(14)
+    z, perm, offsets, weights = ffn_case(rng, 300, 6, 2, 256, 256, torch.bfloat16)
+    d = dims_of(300, 6, 2, 256, 256)
+    zd, pd, od = z.cuda(), gpu(perm), gpu(offsets)
+    want, _ = run_ffn(d, zd, pd, od, weights)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(4)], []
+    for _ in range(5):
+        for st in streams:
+            with torch.cuda.stream(st):
+                outs.append(run_ffn(d, zd, pd, od, weights))
+    torch.cuda.synchronize()
+    for out, ws in outs:
+        assert lm.get_device_status(ws) == lm.OK and torch.equal(out, want)
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second device")
+def test_other_device_is_refused():
+    x = torch.zeros(4, 64, device="cuda:1")
+    with pytest.raises(lm.LmoeError):
+        lm.quantize_rows_fp8(x, torch.zeros(4, 64, dtype=F8, device="cuda:1"),
+                             torch.zeros(1, 4, 4, dtype=torch.uint8, device="cuda:1"))
+
+
+def test_binding_refuses_wrong_tensors():
+    z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="cuda")
+    q, s = z(4, 64, dtype=F8), z(1, 4, 4, dtype=torch.uint8)
+    for bad in ((z(4, 64).half(), q, s), (z(4, 64), z(4, 32, dtype=F8), s), (z(4, 64), q, z(2, 4, 4, dtype=torch.uint8)),
+                (z(64, 4).t(), q, s), (z(4, 66)[:, 1:65], q, s)):
+        with pytest.raises(lm.LmoeError):
+            lm.quantize_rows_fp8(*bad)
+    with pytest.raises(lm.LmoeError):
+        lm.quantize_rows_fp8(z(4, 64), q, s, index=z(4, dtype=torch.int64))
+    d = dims_of(4, 2, 1)
+    w, w_s = z(2, 128, 64, dtype=F8), z(*lm.fp8_weight_scales_shape(2, 128, 64), dtype=torch.uint8)
+    off, out, ws = z(3, dtype=torch.int32), z(4, 128, dtype=torch.bfloat16), lm.alloc_workspace(d)
+    lm.moe_expert_gemm_fp8(d, q, s, off, w, w_s, out, ws)
+    for bad in ((q, s, None, w, w_s, out), (q, s, off, w, w_s, out.float()), (q, s, off, w[:1], w_s, out),
+                (q, s, off.long(), w, w_s, out), (q, s, off, w, w_s, z(128, 4, dtype=torch.bfloat16).t())):
+        with pytest.raises(lm.LmoeError):
+            lm.moe_expert_gemm_fp8(d, *bad, ws)
 
 
 def test_no_tokens():

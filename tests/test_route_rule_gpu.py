@@ -221,6 +221,35 @@ def test_route_backward_floor_strays_and_stride():
         np.testing.assert_allclose(got[t, 3:3 + R], part[0], rtol=64 * U, atol=64 * U)
 
 
+def test_route_forward_and_backward_in_one_graph():
+    """Captured and replayed with new logits, and the same bits as called directly."""
+    rng = np.random.default_rng(31)
+    n, R, k = 130, 96, 6
+    rule, d = rule_of("sigmoid", 8, 4, True, True, 2.5), dims_of(n, R, k)
+    logits, bias = (torch.from_numpy(a).cuda() for a in draw(rng, n, R, k, 0.1, ("sigmoid", 8, 4, True, True, 2.5)))
+    dw = torch.from_numpy(rng.standard_normal((n, k)).astype(np.float32)).cuda()
+    ids, w, dl = (torch.zeros(n, c, dtype=t, device="cuda") for c, t in ((k, torch.int32), (k, torch.float32), (R, torch.float32)))
+
+    def step():
+        lm.moe_route_logits(d, rule, logits, bias, ids, w)
+        lm.moe_route_logits_backward(d, rule, logits, ids, dw, dl)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (32, 33):
+        rng = np.random.default_rng(seed)
+        logits.copy_(torch.from_numpy(rng.standard_normal((n, R)).astype(np.float32)))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in (ids, w, dl)]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, (ids, w, dl)))
+
+
 # ------------------------------------------------------- from x, and together
 @pytest.mark.parametrize("R,groups,kept,k,dtype", [(16, 4, 2, 2, torch.bfloat16), (96, 8, 4, 6, torch.bfloat16),
                                                    (16, 4, 2, 2, torch.float32), (64, 4, 2, 4, torch.float32)])
