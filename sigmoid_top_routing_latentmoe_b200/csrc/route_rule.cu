@@ -135,7 +135,7 @@ constexpr uint32_t kTaken = 0xffffffffu;  // bits of a key that has its slot
 // it (a few dozen) are put in order: each by counting the ones before it, or in
 // k rounds of a warp maximum where k is small.  Clustered keys (more than 64
 // above the bound) and k > 32 take the rounds over every open key.
-template <bool SOFTMAX>
+template <bool SOFTMAX, bool GROUPED>
 __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     const float* __restrict__ logits, int64_t ld, const float* __restrict__ bias, int64_t n, int R,
     int k, Groups g, int renormalise, float scale, int32_t* __restrict__ ids,
@@ -154,10 +154,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
   int* list = reinterpret_cast<int*>(code + g.n);
   uint64_t* cand = cands[warp];
   int* slot_e = slots_e[warp];
-  const bool grouped = g.kept < g.n;
   // R <= 64 without groups: two experts a lane, in registers
-  const bool small = !grouped && R <= 64;
+  const bool small = !GROUPED && R <= 64;
   uint64_t c0 = 0, c1 = 0;  // this lane's candidates
+  float lmax = -INFINITY;   // its largest key (NaN left out)
 
   float top = 0.0f, inv = 0.0f;  // softmax: the largest logit, 1 / sum of the exponentials
   float l0 = -INFINITY, l1 = -INFINITY, bias0 = 0.0f, bias1 = 0.0f;  // small: this lane's
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
   if (SOFTMAX) {
     top = fmaxf(l0, l1);
     if (!small) {
-#pragma unroll 8
+#pragma unroll 16
       for (int e = lane; e < R; e += 32) top = fmaxf(top, lr[e]);
     }
     top = warp_max(top);
@@ -201,23 +201,35 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
       __syncwarp();
     }
   } else {
-#pragma unroll 8
-    for (int e = lane; e < R; e += 32)
-      key[grouped ? e + g.group_of(e) * g.lanes : e] =
-          key_of(lr[e], bias != nullptr ? bias[e] : 0.0f);
+    // whole warps of experts without a check, then the rest
+    const float* lj = lr + lane;
+    const float* bj = bias + lane;
+    const int whole = R >> 5, last = whole * 32 + lane;
+    auto put = [&](int e, float v) {
+      key[GROUPED ? e + g.group_of(e) * g.lanes : e] = v;
+      if (!GROUPED) lmax = fmaxf(lmax, v);
+    };
+    if (bias != nullptr) {
+#pragma unroll 7
+      for (int j = 0; j < whole; ++j) put(j * 32 + lane, key_of(lj[j * 32], bj[j * 32]));
+    } else {
+#pragma unroll 7
+      for (int j = 0; j < whole; ++j) put(j * 32 + lane, key_of(lj[j * 32], 0.0f));
+    }
+    if (last < R) put(last, key_of(lr[last], bias != nullptr ? bias[last] : 0.0f));
     __syncwarp();
-    if (grouped) keep_groups(g, key, code, list);
+    if (GROUPED) keep_groups(g, key, code, list);
   }
 
   // open expert c of `open`: its place among the keys, its number
-  const int open = grouped ? g.kept * g.size : R;
+  const int open = GROUPED ? g.kept * g.size : R;
   auto place = [&](int c) {
-    if (!grouped) return c;
+    if (!GROUPED) return c;
     const int a = g.group_of(c);
     return list[a] * (g.size + g.lanes) + c - a * g.size;
   };
   auto expert = [&](int c) {
-    if (!grouped) return c;
+    if (!GROUPED) return c;
     const int a = g.group_of(c);
     return list[a] * g.size + c - a * g.size;
   };
@@ -231,8 +243,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
       const float l = lr[chosen];
       s = SOFTMAX ? expf(l - top) * inv : sigmoid_f(l);
     }
-    if (renormalise)  // in slot order
-      for (int slot = 0; slot < slots; ++slot) sum += __shfl_sync(kAll, s, slot);
+    if (renormalise) sum += warp_sum(s);
     if (lane < slots) {
       ids_row[base + lane] = chosen;
       if (k <= 32) s = scale * (renormalise ? s / fmaxf(sum, kMinSum) : s);
@@ -242,19 +253,20 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
 
   int total = small ? R : 65;  // candidates
   if (!small && k <= 32) {
-    float least = -INFINITY;  // keys of -inf and NaN count as the lowest finite ones: a superset
+    float least = -INFINITY;  // NaN counts as -inf
     if (open > 64) {
-      float lmax = -INFINITY;
+      if (GROUPED) {
 #pragma unroll 4
-      for (int c = lane; c < open; c += 32) lmax = fmaxf(lmax, fmaxf(key[place(c)], -FLT_MAX));
+        for (int c = lane; c < open; c += 32) lmax = fmaxf(lmax, key[place(c)]);
+      }
       least = decode_key(__shfl_sync(kAll, warp_sort_desc(key_code(lmax)), k - 1));
     }
     total = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int base = 0; base < open; base += 32) {
       const int c = base + lane;
       const float v = c < open ? key[place(c)] : 0.0f;
-      const bool in = c < open && fmaxf(v, -FLT_MAX) >= least;
+      const bool in = c < open && !(v < least) && (v == v || least == -INFINITY);
       const uint32_t m = __ballot_sync(kAll, in);
       if (m == 0) continue;
       const int at = total + __popc(m & ((1u << lane) - 1u));
@@ -411,18 +423,18 @@ int values_per_lane(int R) {
     LMOE_VPL(16, CALL) LMOE_VPL(32, CALL) LMOE_VPL(64, CALL) LMOE_VPL(128, CALL) \
   }
 
-template <bool SOFTMAX>
+template <bool SOFTMAX, bool GROUPED>
 static cudaError_t launch_rule(const RouteRule& rule, const Groups& g, const float* logits,
                                int64_t ld, const float* bias, int64_t n, int R, int k, int32_t* ids,
                                float* probs, cudaStream_t st) {
   const size_t smem = (size_t)kWarps * g.words() * 4;
   if (smem > 40 * 1024) {  // with the candidates' 3 KB, more than a kernel gets unasked
-    cudaError_t e = cudaFuncSetAttribute(route_rule_kernel<SOFTMAX>,
+    cudaError_t e = cudaFuncSetAttribute(route_rule_kernel<SOFTMAX, GROUPED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   count_launch();
-  return launch_pdl(route_rule_kernel<SOFTMAX>, dim3((unsigned)((n + kWarps - 1) / kWarps)),
+  return launch_pdl(route_rule_kernel<SOFTMAX, GROUPED>, dim3((unsigned)((n + kWarps - 1) / kWarps)),
                     dim3(32 * kWarps), smem, st, 1, logits, ld, bias, n, R, k, g, rule.renormalise,
                     rule.scale, ids, probs);
 }
@@ -440,8 +452,10 @@ cudaError_t launch_route_rule(const RouteRule& rule, const float* logits, int64_
   while (g.lanes * 2 * g.n <= 32) g.lanes *= 2;
   g.top2 = rule.top2;
   g.magic = g.size == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + g.size - 1) / g.size);
-  return rule.softmax ? launch_rule<true>(rule, g, logits, ld, bias, n, R, k, ids, probs, st)
-                      : launch_rule<false>(rule, g, logits, ld, bias, n, R, k, ids, probs, st);
+  const bool grouped = g.kept < g.n;
+  const auto run = rule.softmax ? (grouped ? launch_rule<true, true> : launch_rule<true, false>)
+                                : (grouped ? launch_rule<false, true> : launch_rule<false, false>);
+  return run(rule, g, logits, ld, bias, n, R, k, ids, probs, st);
 }
 
 cudaError_t launch_route_rule_backward(const RouteRule& rule, const float* logits, int64_t ld,
