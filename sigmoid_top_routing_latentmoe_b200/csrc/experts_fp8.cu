@@ -38,12 +38,6 @@ constexpr int TMEM_COLS = 512, SF_COL0 = 256;
 static_assert(SF_COL0 + SF_STAGES * SF_COLS <= TMEM_COLS, "TMEM");
 constexpr int EPI_WARP0 = 4, EPI_WARPS = 16, SCALE_WARP0 = EPI_WARP0 + EPI_WARPS, SCALE_WARPS = 4;
 constexpr int THREADS = 32 * (SCALE_WARP0 + SCALE_WARPS);
-// Staging bytes of an epilogue warp.  SiTU stages 32 rows x 32 bytes, in the
-// first half; the second holds the rows' maxima (tile parity, warp of the
-// quarter, quarter and row).
-constexpr int EPI_STAGE = 32 * 64;
-constexpr int SITU_STAGE = 32 * 32, AMAX_BYTES = 2 * 4 * 128 * 4;
-static_assert(SITU_STAGE * EPI_WARPS + AMAX_BYTES <= EPI_STAGE * EPI_WARPS, "staging");
 // The 768 threads start with 80 registers each; the 16 epilogue warps hold 64
 // accumulators a thread and take what the other 8 give up (512 x 96 + 256 x 48
 // = 768 x 80).  Shared memory leaves almost no L1, so a spilled register is read
@@ -59,7 +53,7 @@ template <int CG>
 struct Cfg {
   static constexpr int STAGE_BYTES = A_BYTES + (CG == 1 ? 2 : 1) * SUB_BYTES;
   static constexpr int STAGES = CG == 1 ? 4 : 6;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * EPI_STAGE + 1024;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
 };
 
 struct Params {
@@ -73,6 +67,7 @@ struct Params {
   uint8_t* out_scales;
   int32_t* status;
   float beta1, beta2;
+  int wide_rows;                         // rows of out are 32-byte aligned
 };
 
 // This CTA (or its pair): which of the tiles it takes, and its rank in the pair.
@@ -115,6 +110,7 @@ __device__ __forceinline__ bool two_subs(const Params& p, const Tile& tl) {
 
 struct Sync {
   uint64_t full[6], empty[6], sfull[SF_STAGES], sempty[SF_STAGES], tfull, tempty, drain, quarter[4];
+  float amax[2 * 4 * 128];  // SiTU: maxima by tile parity, warp of the quarter, row
   uint32_t tmem;
   volatile int abort_flag;
 };
@@ -309,38 +305,19 @@ __device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t tmem, Sync& 
   mbar_wait(smem_u32(&s.drain), 0, &no_abort, p.status);
 }
 
-// 16-byte chunk c of this lane's row (32 or 64 bytes) in the warp's staging
-// buffer, XOR-swizzled so that rows written and rows read back are free of
-// bank conflicts.
-template <int BYTES>
-__device__ __forceinline__ uint32_t chunk_at(uint32_t st, int row, int c) {
-  return st + row * BYTES + (BYTES == 64 ? (c ^ ((row >> 1) & 3)) << 4 : (c ^ ((row >> 2) & 1)) << 4);
-}
-template <int BYTES>
-__device__ __forceinline__ void stage_chunk(uint32_t st, int c, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                   chunk_at<BYTES>(st, threadIdx.x & 31, c)),
-               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-// Stores the staged 32 rows x BYTES: `rows` rows, the first `bytes` bytes.
-template <int BYTES>
-__device__ __forceinline__ void flush_rows(uint32_t st, char* base, int64_t ld, int rows, int bytes) {
-  constexpr int CH = BYTES / 16;
-  const int lane = threadIdx.x & 31, c = lane & (CH - 1);
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int row = i * (32 / CH) + lane / CH;
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(chunk_at<BYTES>(st, row, c))
+// Stores 32 bytes of this lane's row at dst, the first `bytes` of them (a
+// multiple of 16): a whole sector in one instruction where rows are 32-byte
+// aligned (wide).  Each lane writes its own row: a transpose through shared
+// memory, for longer runs per instruction, took longer than it saved.
+__device__ __forceinline__ void store32(char* dst, const uint32_t (&w)[8], int bytes, bool wide) {
+  if (wide && bytes >= 32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-    if (row < rows && c * 16 < bytes)
-      *reinterpret_cast<uint4*>(base + (int64_t)row * ld + c * 16) = v;
+  } else {
+    if (bytes >= 16) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (bytes >= 32) *reinterpret_cast<uint4*>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  __syncwarp();
 }
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -446,7 +423,7 @@ __device__ __forceinline__ void situ_units(float& a0, float& a1, float c0, float
 // A tile's hidden units of this warp: 32 rows x 32 units, quantised with the
 // maximum over the row's 128.
 __device__ __forceinline__ void finish_situ(const Params& p, const Tile& tl, float (&v)[64], int rows,
-                                            int quarter, int part, uint32_t st, float* amax,
+                                            int quarter, int part, float* amax,
                                             uint32_t phase, Sync& s, bool& ok) {
   const int lane = threadIdx.x & 31;
   amax += phase * 512 + 32 * quarter + lane;  // of this row: [part * 128]
@@ -485,47 +462,37 @@ __device__ __forceinline__ void finish_situ(const Params& p, const Tile& tl, flo
   for (int i = 0; i < 8; ++i)
     w[i] = pack_e4m3_finite(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
                             v[4 * i + 3] * inv);
-  stage_chunk<32>(st, 0, make_uint4(w[0], w[1], w[2], w[3]));
-  stage_chunk<32>(st, 1, make_uint4(w[4], w[5], w[6], w[7]));
-  const int row0 = tl.m0 + 32 * quarter, col = tl.n * SUB + 32 * part;
-  flush_rows<32>(st, static_cast<char*>(p.out) + (int64_t)row0 * p.n_out + col, p.n_out, rows,
-                 p.n_out - col);
-  if (part == 0 && lane < rows)
-    p.out_scales[((int64_t)(tl.n >> 2) * p.rows + row0 + lane) * 4 + (tl.n & 3)] = (uint8_t)(e + 127);
+  if (lane >= rows) return;
+  const int64_t row = tl.m0 + 32 * quarter + lane;
+  const int col = tl.n * SUB + 32 * part;
+  store32(static_cast<char*>(p.out) + row * p.n_out + col, w, p.n_out - col, p.wide_rows);
+  if (part == 0)
+    p.out_scales[((int64_t)(tl.n >> 2) * p.rows + row) * 4 + (tl.n & 3)] = (uint8_t)(e + 127);
 }
 
 // A plain tile's 32 rows x 64 columns of this warp.
 template <int OUT>
 __device__ __forceinline__ void finish_store(const Params& p, const Tile& tl, const float (&v)[64],
-                                             int rows, int quarter, int part, uint32_t st) {
-  constexpr int ES = OUT == OUT_F32 ? 4 : 2, CB = 64 / ES;  // columns of a 64-byte block
-  const int64_t ld = (int64_t)p.n_out * ES;
-  char* base = static_cast<char*>(p.out) + (int64_t)(tl.m0 + 32 * quarter) * ld;
+                                             int rows, int quarter, int part) {
+  constexpr int ES = OUT == OUT_F32 ? 4 : 2, CB = 32 / ES;  // columns of 32 bytes
+  const int lane = threadIdx.x & 31, col0 = tl.n * 2 * SUB + 64 * part;
+  if (lane >= rows) return;
+  char* row = static_cast<char*>(p.out) + ((int64_t)(tl.m0 + 32 * quarter + lane) * p.n_out + col0) * ES;
 #pragma unroll
   for (int b = 0; b < 64 / CB; ++b) {
-    const int col = tl.n * 2 * SUB + 64 * part + b * CB;
-    if (rows > 0 && col < p.n_out) {
+    const float* f = v + b * CB;
+    uint32_t w[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float* f = v + b * CB + c * (16 / ES);
-        stage_chunk<64>(st, c,
-                        OUT == OUT_F32
-                            ? make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
-                                         __float_as_uint(f[2]), __float_as_uint(f[3]))
-                            : make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
-                                         bf16x2(f[6], f[7])));
-      }
-      flush_rows<64>(st, base + (int64_t)col * ES, ld, rows, (p.n_out - col) * ES);
-    }
+    for (int i = 0; i < 8; ++i)
+      w[i] = OUT == OUT_F32 ? __float_as_uint(f[i]) : bf16x2(f[2 * i], f[2 * i + 1]);
+    store32(row + b * 32, w, (p.n_out - col0 - b * CB) * ES, p.wide_rows);
   }
 }
 
 template <int OUT, int CG>
-__device__ void epilogue(const Params& p, uint32_t tmem, uint8_t* staging, Sync& s, Unit u) {
+__device__ void epilogue(const Params& p, uint32_t tmem, Sync& s, Unit u) {
   const int lane = threadIdx.x & 31, ew = (threadIdx.x >> 5) - EPI_WARP0;
   const int quarter = ew & 3, part = ew >> 2;  // TMEM lanes 32 (warp mod 4) ..., columns
-  const uint32_t st = smem_u32(staging) + ew * (OUT == OUT_SITU ? SITU_STAGE : EPI_STAGE);
-  float* amax = reinterpret_cast<float*>(staging + EPI_WARPS * SITU_STAGE);
   const uint32_t ta = tmem + ((uint32_t)(32 * quarter) << 16);
   // the leader's MMA thread waits for the epilogues of both CTAs
   const uint32_t tempty = CG == 1 ? smem_u32(&s.tempty) : map_to_rank(smem_u32(&s.tempty), 0);
@@ -553,10 +520,10 @@ __device__ void epilogue(const Params& p, uint32_t tmem, uint8_t* staging, Sync&
     }
     if constexpr (OUT == OUT_SITU) {
       bool ok;
-      finish_situ(p, tl, v, rows, quarter, part, st, amax, phase, s, ok);
+      finish_situ(p, tl, v, rows, quarter, part, s.amax, phase, s, ok);
       if (!ok) return;
     } else {
-      finish_store<OUT>(p, tl, v, rows, quarter, part, st);
+      finish_store<OUT>(p, tl, v, rows, quarter, part);
     }
     phase ^= 1u;
   }
@@ -569,7 +536,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Sync s;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* staging = smem_raw + (ring - smem_u32(smem_raw)) + C::STAGES * C::STAGE_BYTES;
   const int warp = threadIdx.x >> 5;
   const Unit u = CG == 1 ? Unit{(int)blockIdx.x, (int)gridDim.x, 0}
                          : Unit{(int)(blockIdx.x >> 1), (int)(gridDim.x >> 1), (int)cluster_rank()};
@@ -608,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp < SCALE_WARP0) {
     regs_inc<REGS_EPI>();
-    epilogue<OUT, CG>(p, tmem, staging, s, u);
+    epilogue<OUT, CG>(p, tmem, s, u);
   } else {
     regs_dec<REGS_OTHER>();
     feed_scales<OUT, CG>(p, tmem, s, u);
@@ -720,6 +686,8 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st) 
   p.out = g.out;
   p.out_scales = g.out_scales;
   p.status = status;
+  const int64_t row_bytes = (int64_t)g.n_out * (g.situ ? 1 : g.out_f32 ? 4 : 2);
+  p.wide_rows = row_bytes % 32 == 0 && reinterpret_cast<uintptr_t>(g.out) % 32 == 0;
   p.beta1 = g.beta1;
   p.beta2 = g.beta2;
   p.n_tiles = g.situ ? p.w_blocks : (g.n_out + 2 * SUB - 1) / (2 * SUB);
