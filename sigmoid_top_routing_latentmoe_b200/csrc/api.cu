@@ -1126,7 +1126,8 @@ lmoe_status moe_expert_gemm_fp8(const lmoe_dims* dims, int32_t n_in, int32_t n_o
   g.n_in = n_in; g.n_out = n_out; g.w = (const uint8_t*)w; g.w_scales = w_scales; g.out = out;
   g.out_f32 = dims->dtype == LMOE_F32 ? 1 : 0;
   g.pairs = pairs;
-  if (offsets != nullptr) {
+  g.offsets = offsets;
+  if (dims->n_routed > 1) {  // a single expert needs no list
     g.tiles = tl.tiles; g.n_mtiles = tl.n_mtiles; g.max_tiles = tl.max_tiles;
     LMOE_CUDA(launch_expert_tiles(tl, st), "expert tiles");
   }

@@ -61,7 +61,8 @@ struct Params {
   const uint32_t* a_words;               // [words, rows]
   const uint32_t *w_words, *w_up_words;  // [R, w_blocks, words]
   int rows, words, w_blocks, kb, n_tiles, n_out;
-  const int4* tiles;
+  const int4* tiles;                     // nullptr: one expert,
+  const int32_t* offsets;                // with its two bounds here, or every row
   const int32_t* n_mtiles;
   void* out;
   uint8_t* out_scales;
@@ -73,19 +74,23 @@ struct Params {
 // This CTA (or its pair): which of the tiles it takes, and its rank in the pair.
 struct Unit {
   int first, step, rank;
+  int lo, hi;  // without a tile list: the only expert's rows
 };
 // A tile, or a CTA's share of its rows: [m0, m0 + rows) of expert e, column tile n.
 struct Tile {
   int e, m0, rows, n;
 };
 template <int CG>
-__device__ __forceinline__ int total_tiles(const Params& p) {
-  return (p.tiles != nullptr ? *p.n_mtiles : (p.rows + BM * CG - 1) / (BM * CG)) * p.n_tiles;
+__device__ __forceinline__ int total_tiles(const Params& p, const Unit& u) {
+  return (p.tiles != nullptr ? *p.n_mtiles : (u.hi - u.lo + BM * CG - 1) / (BM * CG)) * p.n_tiles;
 }
 template <int CG>
-__device__ __forceinline__ Tile decode_tile(const Params& p, int t) {
+__device__ __forceinline__ Tile decode_tile(const Params& p, const Unit& u, int t) {
   const int mt = t / p.n_tiles, n = t - mt * p.n_tiles;
-  if (p.tiles == nullptr) return {0, mt * BM * CG, min(BM * CG, p.rows - mt * BM * CG), n};
+  if (p.tiles == nullptr) {
+    const int m0 = u.lo + mt * BM * CG;
+    return {0, m0, min(BM * CG, u.hi - m0), n};
+  }
   const int4 e = p.tiles[mt];
   return {e.x, e.y, e.z, n};
 }
@@ -93,8 +98,8 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t) {
 // the tile's turn comes (each role waiting for it in turn cost some 1000 cycles
 // a tile); any tile behind the last.
 template <int CG>
-__device__ __forceinline__ Tile tile_ahead(const Params& p, int t, int total) {
-  return t < total ? decode_tile<CG>(p, t) : Tile{0, 0, 0, 0};
+__device__ __forceinline__ Tile tile_ahead(const Params& p, const Unit& u, int t, int total) {
+  return t < total ? decode_tile<CG>(p, u, t) : Tile{0, 0, 0, 0};
 }
 template <int CG>
 __device__ __forceinline__ Tile own_rows(const Tile& t, int rank) {
@@ -123,12 +128,12 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
   int stage = 0;
   uint32_t phase = 0, issued = 0, issued_phase = 0;
   bool ok = true;
-  const int total = total_tiles<CG>(p);
+  const int total = total_tiles<CG>(p, u);
   const uint32_t full0 = smem_u32(s.full), lead0 = CG == 1 ? full0 : map_to_rank(full0, 0);
-  Tile next = tile_ahead<CG>(p, u.first, total);
+  Tile next = tile_ahead<CG>(p, u, u.first, total);
   for (int t = u.first; ok && t < total; t += u.step) {
     const Tile tl = next;
-    next = tile_ahead<CG>(p, t + u.step, total);
+    next = tile_ahead<CG>(p, u, t + u.step, total);
     const bool small = CG == 1 && tl.rows <= SMALL_ROWS, two = two_subs<OUT, CG>(p, tl);
     const CUtensorMap* map_a = small ? &p.tmA32 : &p.tmA;
     // a pair's second CTA loads no A when it has no rows (its accumulator is not stored)
@@ -210,17 +215,17 @@ __device__ __forceinline__ ScaleWords scale_words(const Params& p, const ScaleRo
 template <int OUT, int CG>
 __device__ void feed_scales(const Params& p, uint32_t tmem, Sync& s, Unit u) {
   const int lane = threadIdx.x & 31;
-  const int total = total_tiles<CG>(p);
+  const int total = total_tiles<CG>(p, u);
   const uint32_t full0 = CG == 1 ? smem_u32(s.sfull) : map_to_rank(smem_u32(s.sfull), 0);
   const uint32_t sf0 = tmem + SF_COL0 + ((threadIdx.x & 96) << 16);
   int stage = 0;
   uint32_t phase = 0;
-  Tile tn = own_rows<CG>(tile_ahead<CG>(p, u.first + u.step, total), u.rank);
-  ScaleRows rows = scale_rows<OUT, CG>(p, own_rows<CG>(tile_ahead<CG>(p, u.first, total), u.rank));
+  Tile tn = own_rows<CG>(tile_ahead<CG>(p, u, u.first + u.step, total), u.rank);
+  ScaleRows rows = scale_rows<OUT, CG>(p, own_rows<CG>(tile_ahead<CG>(p, u, u.first, total), u.rank));
   ScaleWords next = scale_words<OUT>(p, rows, 0);
   for (int t = u.first; t < total; t += u.step) {
     const ScaleRows rows1 = scale_rows<OUT, CG>(p, tn);
-    tn = own_rows<CG>(tile_ahead<CG>(p, t + 2 * u.step, total), u.rank);
+    tn = own_rows<CG>(tile_ahead<CG>(p, u, t + 2 * u.step, total), u.rank);
     for (int q = 0; q < p.words; ++q) {
       const ScaleWords w = next;
       if (q + 1 == p.words) rows = rows1;
@@ -254,11 +259,11 @@ __device__ void issue_mmas(const Params& p, uint32_t ring, uint32_t tmem, Sync& 
   int stage = 0, sstage = 0;
   uint32_t phase = 0, sphase = 0, tphase = 0;
   bool ok = true;
-  const int total = total_tiles<CG>(p);
-  Tile next = tile_ahead<CG>(p, u.first, total);
+  const int total = total_tiles<CG>(p, u);
+  Tile next = tile_ahead<CG>(p, u, u.first, total);
   for (int t = u.first; ok && t < total; t += u.step) {
     const bool two = two_subs<OUT, CG>(p, next);
-    next = tile_ahead<CG>(p, t + u.step, total);
+    next = tile_ahead<CG>(p, u, t + u.step, total);
     const uint32_t idesc = instr_desc_mxf8<CG>(two ? 2 * SUB : SUB);
     if (!warp_wait<PAIR>(smem_u32(&s.tempty), tphase ^ 1u, &s.abort_flag, p.status)) break;
     tphase ^= 1u;
@@ -497,11 +502,11 @@ __device__ void epilogue(const Params& p, uint32_t tmem, Sync& s, Unit u) {
   // the leader's MMA thread waits for the epilogues of both CTAs
   const uint32_t tempty = CG == 1 ? smem_u32(&s.tempty) : map_to_rank(smem_u32(&s.tempty), 0);
   uint32_t phase = 0;
-  const int total = total_tiles<CG>(p);
-  Tile next = tile_ahead<CG>(p, u.first, total);
+  const int total = total_tiles<CG>(p, u);
+  Tile next = tile_ahead<CG>(p, u, u.first, total);
   for (int t = u.first; t < total; t += u.step) {
     const Tile tl = own_rows<CG>(next, u.rank);
-    next = tile_ahead<CG>(p, t + u.step, total);
+    next = tile_ahead<CG>(p, u, t + u.step, total);
     const int rows = min(32, tl.rows - 32 * quarter);
     if (!warp_wait(smem_u32(&s.tfull), phase, &s.abort_flag, p.status)) return;
     fence_after();
@@ -537,8 +542,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ Sync s;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5;
-  const Unit u = CG == 1 ? Unit{(int)blockIdx.x, (int)gridDim.x, 0}
-                         : Unit{(int)(blockIdx.x >> 1), (int)(gridDim.x >> 1), (int)cluster_rank()};
+  Unit u = CG == 1 ? Unit{(int)blockIdx.x, (int)gridDim.x, 0, 0, p.rows}
+                   : Unit{(int)(blockIdx.x >> 1), (int)(gridDim.x >> 1), (int)cluster_rank(), 0, p.rows};
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
@@ -564,6 +569,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   // everything above overlaps the previous kernel; inputs are read only below
   pdl_trigger();
   pdl_wait();
+  if (p.offsets != nullptr) {  // clamped, as a tile list would be
+    u.lo = min(max(p.offsets[0], 0), p.rows);
+    u.hi = min(max(p.offsets[1], u.lo), p.rows);
+  }
 
   if (warp < EPI_WARP0) {
     regs_dec<REGS_OTHER>();
@@ -682,6 +691,7 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st) 
   p.kb = q_blocks(g.n_in);
   p.n_out = g.n_out;
   p.tiles = g.tiles;
+  p.offsets = g.tiles == nullptr ? g.offsets : nullptr;
   p.n_mtiles = g.n_mtiles;
   p.out = g.out;
   p.out_scales = g.out_scales;

@@ -61,7 +61,8 @@ struct Fp8Gemm {
   void* out;
   uint8_t* out_scales;
   int out_f32;              // out is fp32, else bf16 (ignored with situ)
-  const int4* tiles;        // nullptr: one expert that has every row
+  const int4* tiles;        // nullptr: one expert, which has the rows
+  const int32_t* offsets;   // [offsets[0], offsets[1]), or every row when that is nullptr
   const int32_t* n_mtiles;
   int max_tiles;
   // CTA pairs over tiles of 256 rows, else single CTAs over tiles of 128; the

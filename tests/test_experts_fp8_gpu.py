@@ -176,6 +176,17 @@ def test_expert_gemm_dense(tiles, rows):
     np.testing.assert_array_equal(got, run_gemm(d, a, a_s, np.array([0, rows], np.int32), w, w_s, 392))
 
 
+@pytest.mark.parametrize("lo,hi", [(0, 0), (5, 300), (-3, 100), (290, 1 << 30), (200, 100)])
+def test_expert_gemm_one_expert_with_bounds(tiles, lo, hi):
+    """A single expert's rows from its two offsets, clamped to the rows there are."""
+    rng = np.random.default_rng(15)
+    av, a, a_s = quantized_rows(rng, 300, 256)
+    wv, w, w_s = quantized_weights(rng, 1, 264, 256)
+    got = run_gemm(dims_of(300, 1, 1), a, a_s, np.array([lo, hi], np.int32), w, w_s, 264)
+    lo = min(max(lo, 0), 300)
+    check_gemm(got, av, wv, [lo, min(max(hi, lo), 300)], torch.bfloat16)
+
+
 def test_expert_gemm_rows_of_no_expert(tiles):
     rng = np.random.default_rng(5)
     av, a, a_s = quantized_rows(rng, 400, 256)
