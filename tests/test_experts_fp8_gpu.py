@@ -309,6 +309,21 @@ def test_expert_ffn_wide_activations(tiles):
     check_ffn(out.double().cpu().numpy(), z, perm, offsets, weights, torch.bfloat16, 2.0, 7.0)
 
 
+def test_expert_ffn_nan_stays_in_its_rows(tiles):
+    """A NaN (or an infinity, which 8 bits do not hold) in a token reaches its pairs only."""
+    rng = np.random.default_rng(16)
+    z, perm, offsets, weights = ffn_case(rng, 90, 3, 2, 256, 272, torch.bfloat16)
+    z[17, 3], z[40, 200] = float("nan"), float("inf")
+    out, ws = run_ffn(dims_of(90, 3, 2, 256, 272), z.cuda(), gpu(perm), gpu(offsets), weights)
+    assert lm.get_device_status(ws) == lm.OK
+    got = out.double().cpu().numpy()
+    bad = np.isin(perm, (17, 40))
+    assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
+    z[17], z[40] = 0.0, 0.0
+    want, bound = ref.ffn(z.double().numpy(), perm, offsets, *[v for v, _, _ in weights], 4.0, 25.0)
+    assert (np.abs(got - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound))[~bad].all()
+
+
 def test_expert_ffn_dropped_rows_and_stray_tokens(tiles):
     """Sorted slots behind the last expert keep what they held; perm entries there are not read as rows."""
     rng = np.random.default_rng(4)
