@@ -31,7 +31,11 @@ using namespace tc;
 
 constexpr int BM = 128, SUB = 128, BK = 128;
 constexpr int A_BYTES = BM * BK, SUB_BYTES = SUB * BK;
-constexpr int SMALL_ROWS = 32;            // tiles of at most this many rows load a smaller A box
+// Heights of the boxes of A on single CTAs: a tile loads the smallest that holds
+// its rows.  The rows of shared memory behind a small box start as zeros: the
+// MMAs multiply all 128, and on a decode step that many empty rows of leftover
+// data drew the GPU to its power cap (LATER).
+constexpr int BOX8 = 8, BOX32 = 32;
 constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
 constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
 constexpr int TMEM_COLS = 512, SF_COL0 = 256;
@@ -57,7 +61,7 @@ struct Cfg {
 };
 
 struct Params {
-  CUtensorMap tmA, tmA32, tmB0, tmB1;
+  CUtensorMap tmA, tmA32, tmA8, tmB0, tmB1;
   const uint32_t* a_words;               // [words, rows]
   const uint32_t *w_words, *w_up_words;  // [R, w_blocks, words]
   int rows, words, w_blocks, kb, n_tiles, n_out;
@@ -135,12 +139,13 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
   for (int t = u.first; ok && t < total; t += u.step) {
     const Tile tl = next;
     next = tile_ahead<CG>(p, u, t + u.step, total);
-    const bool small = CG == 1 && tl.rows <= SMALL_ROWS, two = two_subs<OUT, CG>(p, tl);
-    const CUtensorMap* map_a = small ? &p.tmA32 : &p.tmA;
+    const bool two = two_subs<OUT, CG>(p, tl);
+    const int box = CG == 2 || tl.rows > BOX32 ? BM : tl.rows > BOX8 ? BOX32 : BOX8;
+    const CUtensorMap* map_a = box == BM ? &p.tmA : box == BOX32 ? &p.tmA32 : &p.tmA8;
     // a pair's second CTA loads no A when it has no rows (its accumulator is not stored)
     const bool load_a = u.rank == 0 || tl.rows > BM;
     const int a_ctas = CG == 2 && tl.rows > BM ? 2 : 1;
-    const uint32_t bytes = a_ctas * (small ? SMALL_ROWS * BK : A_BYTES) + (two ? 2 : 1) * SUB_BYTES;
+    const uint32_t bytes = a_ctas * box * BK + (two ? 2 : 1) * SUB_BYTES;
     // this CTA's boxes of W: gate and up, or two neighbouring boxes; of a pair, each CTA one
     const int row0 = tl.n * p.bn;
     const int row1 = OUT == OUT_SITU ? row0 : row0 + SUB;
@@ -562,6 +567,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CG>(smem_u32(&s.tmem), TMEM_COLS);
+  if (CG == 1)
+    for (int i = 0; i < C::STAGES; ++i)
+      for (int b = threadIdx.x * 16; b < A_BYTES; b += THREADS * 16)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i * C::STAGE_BYTES + b), "r"(0)
+                     : "memory");
+  fence_async_smem();  // before TMA writes there, and the MMAs read
   fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();  // both CTAs' barriers exist before any remote arrive
@@ -679,7 +690,8 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, int32_t* status, cudaStream_t st) 
   if (g.rows == 0) return cudaSuccess;
   Params p{};
   bool ok = make_map(&p.tmA, g.a, g.n_in, g.rows, 1, BM, 2) &&
-            make_map(&p.tmA32, g.a, g.n_in, g.rows, 1, SMALL_ROWS, 2) &&
+            make_map(&p.tmA32, g.a, g.n_in, g.rows, 1, BOX32, 2) &&
+            make_map(&p.tmA8, g.a, g.n_in, g.rows, 1, BOX8, 2) &&
             make_map(&p.tmB0, g.w, g.n_in, g.n_out, g.R, SUB, 3) &&
             (!g.situ || make_map(&p.tmB1, g.w_up, g.n_in, g.n_out, g.R, SUB, 3));
   if (!ok) return cudaErrorInvalidValue;

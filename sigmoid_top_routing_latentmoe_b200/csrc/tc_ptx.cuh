@@ -162,6 +162,10 @@ __device__ __forceinline__ void fence_before() {
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// Shared-memory writes of this thread become visible to the async proxy.
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 // Arrive, when this thread's MMAs are complete, on the barrier at this offset
 // (CG = 2: in both CTAs of the pair).
 template <int CG>
