@@ -277,9 +277,13 @@ typedef struct {
 /* moe_expert_ffn with 8-bit products: the rows z[perm_token[r]] are quantised,
  * a and c are products with W_g and W_u, the hidden units (in fp32) are
  * quantised, and expert_out is the product with W_o, in the activation dtype.
- * Rows in no expert's range are left as they are.  latent and ff_routed
- * multiples of 16.  z, perm_token, offsets, expert_out and the workspace as
- * for moe_expert_ffn. */
+ * Rows in no expert's range are left as they are; a perm_token entry outside
+ * [0, N) counts as a token of zeros.  latent and ff_routed multiples of 16.  z,
+ * perm_token, offsets, expert_out and the workspace as for moe_expert_ffn.
+ * Both 8-bit products run on CTA pairs (tiles of 256 rows) or single CTAs (128)
+ * by the average rows per expert, K and the number of tiles; the environment
+ * variable LMOE_FP8_PAIRS=0 or 1 chooses.  Results are the same bits on every
+ * call with the same arguments. */
 LMOE_API lmoe_status moe_expert_ffn_fp8(const lmoe_dims* dims, const void* z,
                                         const int32_t* perm_token, const int32_t* offsets,
                                         const lmoe_fp8_experts* weights, void* expert_out, void* ws,

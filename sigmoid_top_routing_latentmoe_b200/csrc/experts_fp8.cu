@@ -34,7 +34,8 @@ constexpr int A_BYTES = BM * BK, SUB_BYTES = SUB * BK;
 // Heights of the boxes of A on single CTAs: a tile loads the smallest that holds
 // its rows.  The rows of shared memory behind a small box start as zeros: the
 // MMAs multiply all 128, and on a decode step that many empty rows of leftover
-// data drew the GPU to its power cap (LATER).
+// data drew the GPU to its power cap (K3 width, 64 tokens: 645 us, 580 with
+// zeros).
 constexpr int BOX8 = 8, BOX32 = 32;
 constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
 constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
