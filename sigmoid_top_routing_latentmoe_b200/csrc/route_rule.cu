@@ -8,7 +8,6 @@
 // Ties go to the lower group and the lower expert; a key that is NaN ranks
 // with -inf, so that every row has k distinct experts.  b only selects.
 #include <algorithm>
-#include <cfloat>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -78,10 +77,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // banks), the groups' codes and the kept groups in ascending order.
 struct Groups {
   int n, kept, size, lanes, top2;  // lanes: how many lanes scan one group (a power of two)
-  uint32_t magic;                  // ceil(2^32 / size): e / size = umulhi(e, magic) for e < 4096
+  uint32_t magic;                  // ceil(2^32 / size): e / size = umulhi(e, magic) for e < 4096, size > 1
   __host__ __device__ int key_words() const { return n * (size + lanes); }
   __host__ __device__ int words() const { return key_words() + 2 * n; }
-  __device__ int group_of(int e) const { return size == 1 ? e : (int)__umulhi((uint32_t)e, magic); }
+  __device__ int group_of(int e) const { return (int)__umulhi((uint32_t)e, magic); }
 };
 
 // Puts the topk_groups best groups in ascending order into `list`.
@@ -106,7 +105,7 @@ __device__ __forceinline__ void keep_groups(const Groups& g, const float* key, u
       b = fmaxf(fminf(a, oa), fmaxf(b, ob));
       a = fmaxf(a, oa);
     }
-    if (gi < g.n && sub == 0) code[gi] = key_code(g.top2 && g.size > 1 ? a + b : a);
+    if (gi < g.n && sub == 0) code[gi] = key_code(g.top2 ? a + b : a);
   }
   __syncwarp();
   int kept = 0;
@@ -446,7 +445,10 @@ cudaError_t launch_route_rule(const RouteRule& rule, const float* logits, int64_
   Groups g;
   g.n = rule.n_groups;
   g.kept = rule.topk_groups;
-  if (g.kept == g.n) g.n = g.kept = 1;  // every group is kept: as one
+  // Every group is kept: as one.  So are groups of one expert: the top_k keys of
+  // the topk_groups >= top_k best groups are the top_k keys, ties included (4096
+  // of them would need 256 KB of shared memory a block).
+  if (g.kept == g.n || g.n == R) g.n = g.kept = 1;
   g.size = R / g.n;
   g.lanes = 1;
   while (g.lanes * 2 * g.n <= 32) g.lanes *= 2;

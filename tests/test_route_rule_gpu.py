@@ -135,6 +135,23 @@ def test_route_lowest_finite_values():
         np.testing.assert_allclose(got_w, w, rtol=64 * U, atol=0)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_groups_of_one_expert(score):
+    """As many groups as experts, to the largest number: the same as no groups, NaN and ties included."""
+    rng = np.random.default_rng(41)
+    for R, k, kept in ((4096, 32, 4095), (4096, 7, 7), (3600, 40, 50), (2, 1, 1)):
+        logits = np.stack([rng.permutation(np.linspace(-3, 3, R)) for _ in range(6)]).astype(np.float32)
+        logits[1] = 0.0
+        if R > 2:
+            logits[2, 5:9] = np.nan if score == "sigmoid" else -np.inf
+        l = torch.from_numpy(logits).cuda()
+        got = run_route(l, None, k, rule_of(score, R, kept))
+        want = run_route(l, None, k, rule_of(score))
+        np.testing.assert_array_equal(got[0], want[0])
+        np.testing.assert_array_equal(got[1], want[1])
+        np.testing.assert_array_equal(got[0], ref.route(logits, None, k, score, R, kept)[0])
+
+
 # --------------------------------------------------------------- gradient
 def backward_ref(logits, ids, dw, score, renorm, scale):
     s = ref.route_keys(logits, None, score)[0]
