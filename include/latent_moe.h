@@ -165,7 +165,7 @@ LMOE_API lmoe_status moe_route_logits(const lmoe_dims* dims, const lmoe_route_ru
  * <dprobs, probs> for the routing ids [N, k] (each row k distinct experts, as
  * the forward gives them; an id outside [0, R) adds nothing).  The choice of
  * experts is not differentiated; where sum_T s is at its floor, the floor is a
- * constant.  Deterministic. */
+ * constant.  dlogits shares no element with logits (refused).  Deterministic. */
 LMOE_API lmoe_status moe_route_logits_backward(const lmoe_dims* dims, const lmoe_route_rule* rule,
                                                const float* logits, int64_t ld, const int32_t* ids,
                                                const float* dprobs, float* dlogits, int64_t ld_d,

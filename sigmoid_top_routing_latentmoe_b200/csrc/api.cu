@@ -994,6 +994,17 @@ lmoe_status moe_route_logits(const lmoe_dims* dims, const lmoe_route_rule* rule,
   return LMOE_OK;
 }
 
+// Whether two fp32 matrices [n, R] share an element: exact for equal row
+// strides, by their ranges for others.
+static bool matrices_overlap(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t n,
+                             int R) {
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  if (a0 >= b0 + ((n - 1) * ldb + R) * 4 || b0 >= a0 + ((n - 1) * lda + R) * 4) return false;
+  if (lda != ldb || n == 1) return true;
+  const int64_t shift = (int64_t)((a0 > b0 ? a0 - b0 : b0 - a0) / 4) % lda;
+  return shift < R || shift > lda - R;
+}
+
 lmoe_status moe_route_logits_backward(const lmoe_dims* dims, const lmoe_route_rule* rule,
                                       const float* logits, int64_t ld, const int32_t* ids,
                                       const float* dprobs, float* dlogits, int64_t ld_d,
@@ -1004,6 +1015,8 @@ lmoe_status moe_route_logits_backward(const lmoe_dims* dims, const lmoe_route_ru
   LMOE_TRY(check_logits(dims, logits, ld, "logits"));
   LMOE_TRY(check_logits(dims, dlogits, ld_d, "dlogits"));
   if (dims->n_tokens > 0) {
+    if (matrices_overlap(logits, ld, dlogits, ld_d, dims->n_tokens, dims->n_routed))
+      return fail(LMOE_EINVAL, "dlogits overlaps the logits");
     LMOE_PTR(ids, "ids");
     LMOE_PTR(dprobs, "dprobs");
   }

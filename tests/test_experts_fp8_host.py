@@ -105,3 +105,24 @@ def test_scale_shapes():
     assert lm.fp8_row_scales_shape(5, 16) == (1, 5, 4)
     assert lm.fp8_row_scales_shape(5, 528) == (2, 5, 4)
     assert lm.fp8_weight_scales_shape(3, 129, 512) == (3, 2, 4)
+
+
+def test_backward_refuses_a_gradient_over_the_logits():
+    """The gradient is written before the last logits are read: a call in place would be wrong.
+    Matrices beside each other in the columns of one buffer do not overlap."""
+    r, n, R = rule(), 8, 24
+    def back(logits, ld, dlogits, ldd, n=n):
+        dims = lm.make_dims(n, 64, 128, R, 4, 0, 256, 0)
+        status = lm._lib.moe_route_logits_backward(ctypes.byref(dims), ctypes.byref(r), logits, ld, None, None,
+                                                   dlogits, ldd, None)
+        assert status == lm.EINVAL               # without ids no call gets as far as a launch
+        return b"overlap" in lm._lib.lmoe_last_error()
+    def touch(a, lda, b, ldb):   # shared elements, counted one by one
+        at = lambda p, ld: {p // 4 + t * ld + e for t in range(n) for e in range(R)}
+        return bool(at(a, lda) & at(b, ldb))
+    for shift in (0, 4, 4 * 23, 4 * 24, 4 * 26, 4 * 27, 4 * 49, 4 * 50, 4 * 51, 4 * (7 * 50 + 23), 4 * (7 * 50 + 24)):
+        for a, b in ((FAKE, FAKE + shift), (FAKE + shift, FAKE)):
+            assert back(a, 50, b, 50) == touch(a, 50, b, 50), (shift, a < b)
+    assert back(FAKE, 24, FAKE, 24) and not back(FAKE, 24, FAKE + 4 * 24 * n, 24)
+    assert back(FAKE, 24, FAKE + 4 * 24 * (n - 1), 30)      # other strides: the ranges decide
+    assert back(FAKE, 24, FAKE, 24, n=1) and not back(FAKE, 24, FAKE + 4 * 24, 24, n=1)
