@@ -321,8 +321,8 @@ static lmoe_status run_route_grouped(const lmoe_dims* d, const RouteRule& rule, 
 // Tiles of an 8-bit product: CTA pairs over 256 rows when experts have more than
 // 128 rows on average, K is at least 512 long and the tiles fill the pairs once;
 // else single CTAs over 128 rows.  Measured (FFN, single / pairs): mid layer with
-// 2048 rows an expert 467 / 428 us, with 128 rows 67.6 / 71.7; K3 width with 146
-// rows 960 / 900 us, with 37 rows 872 / 1182; 0.5b layer (l = 384) with 512 rows
+// 2048 rows an expert 463 / 432 us, with 128 rows 69.6 / 73.7; K3 width with 146
+// rows 1514 / 1460 us, with 37 rows 850 / 1140; 0.5b layer (l = 384) with 512 rows
 // 32.8 / 38.9.  LMOE_FP8_PAIRS=0 or 1 overrides it.
 static bool fp8_pairs(const lmoe_dims* d, int n_in, int n_out) {
   if (const char* v = getenv("LMOE_FP8_PAIRS")) {
@@ -347,7 +347,7 @@ static TileList tile_list(const lmoe_dims* d, const Layout& L, const int32_t* of
 
 // The rows of z in sorted order: with little to quantise in one kernel through
 // perm, else quantised once per token and then sorted in 8 bits (131072 rows of
-// 3584: 227 us in one kernel, 120 us in two).
+// 3584: 227 us in one kernel, 119 to 139 us in two).
 static bool fp8_sorts(const lmoe_dims* d) {
   return d->top_k > 1 && d->n_tokens * (int64_t)d->top_k * d->latent >= (int64_t)1 << 24;
 }

@@ -134,6 +134,8 @@ constexpr uint32_t kTaken = 0xffffffffu;  // bits of a key that has its slot
 // it (a few dozen) are put in order: each by counting the ones before it, or in
 // k rounds of a warp maximum where k is small.  Clustered keys (more than 64
 // above the bound) and k > 32 take the rounds over every open key.
+// Bound by issue slots (68 %), not bytes: 8192 x 896, top 16, takes 25 us in 14
+// groups and 20 without, 4.7 us at the copy rate; 64 tokens take one warp's chain, 7 us.
 template <bool SOFTMAX, bool GROUPED>
 __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     const float* __restrict__ logits, int64_t ld, const float* __restrict__ bias, int64_t n, int R,
@@ -337,6 +339,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
 //   weights do not change when every selected score is scaled, so c = 0 there
 //   (unless D is the floor).
 // A sigmoid row reads the k selected logits only.
+// Bound by bytes: 8192 x 896 takes 10.6 us softmax (9.2 at the copy rate), 7.5 sigmoid.
 template <int VPL, bool SOFTMAX>
 __global__ void __launch_bounds__(32 * kWarps) route_rule_backward_kernel(
     const float* __restrict__ logits, int64_t ld, const int32_t* __restrict__ ids,
