@@ -31,11 +31,12 @@ using namespace tc;
 
 constexpr int BM = 128, SUB = 128, BK = 128;
 constexpr int A_BYTES = BM * BK, SUB_BYTES = SUB * BK;
-// Heights of the boxes of A on single CTAs: a tile loads the smallest that holds
-// its rows.  The rows of shared memory behind a small box start as zeros: the
+// Heights of the boxes of A: a CTA loads the smallest that holds its rows of a
+// tile.  The rows of shared memory behind a small box start as zeros: the
 // MMAs multiply all 128, and on a decode step that many empty rows of leftover
 // data drew the GPU to its power cap (K3 width, 64 tokens: 645 us, 580 with
-// zeros).
+// zeros).  On pairs each CTA has its own box: K3 width, 8192 tokens evenly
+// spread (146 rows an expert) 1437 -> 1405 us.
 constexpr int BOX8 = 8, BOX32 = 32;
 constexpr int SF_STAGES = 4;              // scale stages, each four K blocks
 constexpr int SF_COLS = 16;               // TMEM columns of a scale stage (4 + 8 used)
@@ -128,6 +129,11 @@ struct Sync {
 static_assert(Cfg<1>::SMEM_BYTES + sizeof(Sync) <= 232448 &&
                   Cfg<2>::SMEM_BYTES + sizeof(Sync) <= 232448, "shared memory");
 
+// Rows of the box of A that a CTA loads for the rows it has.
+__device__ __forceinline__ int box_rows(int rows) {
+  return rows > BOX32 ? BM : rows > BOX8 ? BOX32 : BOX8;
+}
+
 template <int OUT, int CG>
 __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
   using C = Cfg<CG>;
@@ -141,12 +147,13 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
     const Tile tl = next;
     next = tile_ahead<CG>(p, u, t + u.step, total);
     const bool two = two_subs<OUT, CG>(p, tl);
-    const int box = CG == 2 || tl.rows > BOX32 ? BM : tl.rows > BOX8 ? BOX32 : BOX8;
+    const int box = box_rows(tl.rows - BM * u.rank);
     const CUtensorMap* map_a = box == BM ? &p.tmA : box == BOX32 ? &p.tmA32 : &p.tmA8;
     // a pair's second CTA loads no A when it has no rows (its accumulator is not stored)
     const bool load_a = u.rank == 0 || tl.rows > BM;
-    const int a_ctas = CG == 2 && tl.rows > BM ? 2 : 1;
-    const uint32_t bytes = a_ctas * box * BK + (two ? 2 : 1) * SUB_BYTES;
+    // of the whole tile; the leader's barrier counts both CTAs' boxes
+    const int a_rows = box_rows(tl.rows) + (CG == 2 && tl.rows > BM ? box_rows(tl.rows - BM) : 0);
+    const uint32_t bytes = a_rows * BK + (two ? 2 : 1) * SUB_BYTES;
     // this CTA's boxes of W: gate and up, or two neighbouring boxes; of a pair, each CTA one
     const int row0 = tl.n * p.bn;
     const int row1 = OUT == OUT_SITU ? row0 : row0 + SUB;
@@ -568,11 +575,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CG>(smem_u32(&s.tmem), TMEM_COLS);
-  if (CG == 1)
-    for (int i = 0; i < C::STAGES; ++i)
-      for (int b = threadIdx.x * 16; b < A_BYTES; b += THREADS * 16)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i * C::STAGE_BYTES + b), "r"(0)
-                     : "memory");
+  for (int i = 0; i < C::STAGES; ++i)
+    for (int b = threadIdx.x * 16; b < A_BYTES; b += THREADS * 16)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i * C::STAGE_BYTES + b), "r"(0)
+                   : "memory");
   fence_async_smem();  // before TMA writes there, and the MMAs read
   fence_before();
   __syncthreads();
