@@ -322,7 +322,7 @@ static lmoe_status run_route_grouped(const lmoe_dims* d, const RouteRule& rule, 
 // 128 rows on average, K is at least 512 long and the tiles fill the pairs once;
 // else single CTAs over 128 rows.  Measured (FFN, single / pairs): mid layer with
 // 2048 rows an expert 463 / 432 us, with 128 rows 69.6 / 73.7; K3 width with 146
-// rows 1514 / 1460 us, with 37 rows 850 / 1140; 0.5b layer (l = 384) with 512 rows
+// rows 1498 / 1405 us, with 37 rows 850 / 1140; 0.5b layer (l = 384) with 512 rows
 // 32.8 / 38.9.  LMOE_FP8_PAIRS=0 or 1 overrides it.
 static bool fp8_pairs(const lmoe_dims* d, int n_in, int n_out) {
   if (const char* v = getenv("LMOE_FP8_PAIRS")) {
