@@ -134,7 +134,8 @@ LMOE_API lmoe_status moe_route(const lmoe_dims* dims, const void* x, const void*
  *   p_i   = scale * s_i / max(sum_T s, 1e-9) with renormalise, else scale * s_i
  * Ties go to the lower group and the lower expert.  A key that is NaN ranks
  * with -inf (so that the ids of a row are always k distinct experts); its
- * weight stays NaN.  Logits of -inf have score 0, also where every logit of a
+ * weight stays NaN, with renormalise every weight of the row (and the gradient
+ * of every expert chosen there).  Logits of -inf have score 0, also where every logit of a
  * row is -inf.  A bias of -inf closes an expert: it is chosen only when the
  * kept groups hold fewer than k others. */
 typedef enum { LMOE_SCORE_SIGMOID = 0, LMOE_SCORE_SOFTMAX = 1 } lmoe_score;

@@ -20,6 +20,10 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kMinSum = 1e-9f;  // the least sum that weights are divided by
 constexpr int kWarps = 4;
 
+// What weights are divided by.  A NaN stays one (fmaxf would give the floor, and
+// the row's other weights 1e9 times their score).
+__device__ __forceinline__ float divisor(float sum) { return sum < kMinSum ? kMinSum : sum; }
+
 __device__ __forceinline__ float sigmoid_f(float l) { return 1.0f / (1.0f + expf(-l)); }
 
 // Order-preserving code of a key, above 0 for every key: -0 counts as 0, NaN as -inf.
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     if (renormalise) sum += warp_sum(s);
     if (lane < slots) {
       ids_row[base + lane] = chosen;
-      if (k <= 32) s = scale * (renormalise ? s / fmaxf(sum, kMinSum) : s);
+      if (k <= 32) s = scale * (renormalise ? s / divisor(sum) : s);
       probs_row[base + lane] = s;
     }
   };
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
   }
   if (k > 32)  // each lane's own values
     for (int slot = lane; slot < k; slot += 32)
-      probs_row[slot] = scale * (renormalise ? probs_row[slot] / fmaxf(sum, kMinSum)
+      probs_row[slot] = scale * (renormalise ? probs_row[slot] / divisor(sum)
                                              : probs_row[slot]);
 }
 
@@ -386,8 +390,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_backward_kernel(
   }
   sum_s = warp_sum(sum_s);
   sum_gs = warp_sum(sum_gs);
-  const float d = fmaxf(sum_s, kMinSum);
-  const bool floored = !(sum_s > kMinSum);
+  const float d = divisor(sum_s);
+  const bool floored = sum_s <= kMinSum;
   const float mean = renormalise && !floored ? sum_gs / d : 0.0f;
   const float c = !SOFTMAX || (renormalise && !floored) ? 0.0f : renormalise ? sum_gs / d : sum_gs;
 #pragma unroll
