@@ -8,6 +8,7 @@
 // Ties go to the lower group and the lower expert; a key that is NaN ranks
 // with -inf, so that every row has k distinct experts.  b only selects.
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -429,14 +430,37 @@ int values_per_lane(int R) {
     LMOE_VPL(16, CALL) LMOE_VPL(32, CALL) LMOE_VPL(64, CALL) LMOE_VPL(128, CALL) \
   }
 
+// Dynamic shared memory that the rule kernels may need: 4096 experts in 2048
+// groups of two.  The limit of a kernel is raised to it once per device: set to
+// each call's own size, one host thread could lower it between another's setting
+// and its launch.
+constexpr int kMaxExperts = 4096, kMaxDevices = 64;
+constexpr int kMaxSmem = kWarps * 4 * (kMaxExperts + 3 * (kMaxExperts / 2));
+
+template <bool SOFTMAX, bool GROUPED>
+static cudaError_t raise_smem_limit() {
+  static std::mutex mu;
+  static bool raised[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!raised[dev]) {
+    e = cudaFuncSetAttribute(route_rule_kernel<SOFTMAX, GROUPED>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    raised[dev] = e == cudaSuccess;
+  }
+  return e;
+}
+
 template <bool SOFTMAX, bool GROUPED>
 static cudaError_t launch_rule(const RouteRule& rule, const Groups& g, const float* logits,
                                int64_t ld, const float* bias, int64_t n, int R, int k, int32_t* ids,
                                float* probs, cudaStream_t st) {
   const size_t smem = (size_t)kWarps * g.words() * 4;
   if (smem > 40 * 1024) {  // with the candidates' 3 KB, more than a kernel gets unasked
-    cudaError_t e = cudaFuncSetAttribute(route_rule_kernel<SOFTMAX, GROUPED>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = raise_smem_limit<SOFTMAX, GROUPED>();
     if (e != cudaSuccess) return e;
   }
   count_launch();

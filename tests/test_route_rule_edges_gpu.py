@@ -1,4 +1,8 @@
-"""Routing under a rule where it can go wrong: a NaN among the chosen experts."""
+"""Routing under a rule where it can go wrong: a NaN among the chosen experts, calls from
+several host threads at once."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -98,3 +102,31 @@ def test_nan_among_the_chosen_backward(R, k, groups, kept, score, renorm):
         want = chosen if renorm else chosen & np.isnan(logits[t])
         np.testing.assert_array_equal(np.isnan(got[t]), want)
         assert (got[t][~chosen] == 0.0).all()
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_host_threads_side_by_side(grouped):
+    """Calls of two sizes, both with more shared memory than a kernel gets unasked, from four threads."""
+    k, results = 5, []
+
+    def work(R):
+        rng = np.random.default_rng(R)
+        logits = np.stack([rng.permutation(np.linspace(-3, 3, R)) for _ in range(3)]).astype(np.float32)
+        groups, kept = (R // 2, 9) if grouped else (1, 1)
+        rule, d, l = rule_of("sigmoid", groups, kept), dims_of(3, R, k), torch.from_numpy(logits).cuda()
+        ids, w = torch.zeros(3, k, dtype=torch.int32, device="cuda"), torch.zeros(3, k, device="cuda")
+        stream = torch.cuda.Stream()
+        args = (ctypes.byref(d), ctypes.byref(rule), l.data_ptr(), R, None, ids.data_ptr(), w.data_ptr(),
+                stream.cuda_stream)
+        torch.cuda.synchronize()
+        refused = sum(lm._lib.moe_route_logits(*args) != lm.OK for _ in range(5000))
+        stream.synchronize()
+        want = ref.route(logits, None, k, "sigmoid", groups, kept)[0]
+        results.append((R, refused, bool((ids.cpu().numpy() == want).all())))
+
+    threads = [threading.Thread(target=work, args=(R,)) for R in (4096, 2600, 4096, 2600)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sorted(results) == [(2600, 0, True)] * 2 + [(4096, 0, True)] * 2, results
