@@ -254,8 +254,9 @@ LMOE_API lmoe_status lmoe_quantize_weights_fp8(const void* w, int32_t dtype, int
  *   w [R, n_out, n_in], w_scales: as lmoe_quantize_weights_fp8 writes them
  *   out [N*k, n_out] in the activation dtype; rows in no expert's range are
  *   left as they are
- * n_in a multiple of 16, n_out of 8.  Offsets are clamped to an ascending
- * order in [0, N*k].  With the transposed weights and scales it gives the
+ * n_in a multiple of 16, n_out of 8.  Offsets are clamped to [0, N*k], and to
+ * the largest before them where they do not ascend, so that no row has two
+ * experts.  With the transposed weights and scales it gives the
  * gradient of the rows (the weights being constants).  Workspace:
  * lmoe_workspace_size(dims) bytes (of dims: n_tokens, top_k, n_routed, dtype
  * matter here). */

@@ -82,44 +82,50 @@ __device__ __forceinline__ void quantize_vec(const uint4& v, float inv, uint32_t
   }
 }
 
-// The tile list of a ragged product: expert e's rows [offsets[e], offsets[e + 1])
-// in tiles of at most tile_m.  Offsets are clamped to an ascending order inside
-// [0, rows] and the list to max_tiles, so that no list leads a product out of
-// its buffers.  One block of kTileThreads; a block-wide scan over as many experts
-// at a time.
+// The tile list of a ragged product: expert e's rows [bound[e], bound[e + 1]) in
+// tiles of at most tile_m.  bound[e] is the largest of offsets[0 ... e] clamped to
+// [0, rows]: the offsets themselves where they ascend, as a dispatch gives them,
+// and otherwise still an order in which no row belongs to two experts (two tiles
+// would write it, in either order) and the list fits into max_tiles.  One block
+// of kTileThreads; block-wide scans over as many experts at a time.
 constexpr int kTileThreads = 256;
-__device__ __forceinline__ void build_tile_list(const TileList& t) {
-  __shared__ int warp_sum[kTileThreads / 32];
+// Inclusive scan over the block; `part` gets the warps' totals.
+template <bool MAX>
+__device__ __forceinline__ int block_scan(int v, int* part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int base = 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v = MAX ? max(v, o) : v + o;
+  }
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kTileThreads / 32; ++w)
+    if (w < warp) v = MAX ? max(v, part[w]) : v + part[w];
+  return v;
+}
+__device__ __forceinline__ void build_tile_list(const TileList& t) {
+  __shared__ int warp_max[kTileThreads / 32], warp_sum[kTileThreads / 32];
+  __shared__ int bounds[kTileThreads + 1];
+  const int rows = (int)t.rows;
+  int base = 0, start = min(max(t.offsets[0], 0), rows);  // tiles and rows of the experts before
   for (int e0 = 0; e0 < t.R; e0 += kTileThreads) {
     const int e = e0 + threadIdx.x;
-    int lo = 0, hi = 0;
-    if (e < t.R) {
-      lo = (int)min((int64_t)max(t.offsets[e], 0), t.rows);
-      hi = (int)min((int64_t)max(t.offsets[e + 1], lo), t.rows);
-    }
-    const int n = (hi - lo + t.tile_m - 1) / t.tile_m;
-    int inc = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
+    const int end = e < t.R ? min(t.offsets[e + 1], rows) : 0;
+    const int hi = max(start, block_scan<true>(end, warp_max));
+    bounds[threadIdx.x + 1] = hi;
+    if (threadIdx.x == 0) bounds[0] = start;
     __syncthreads();
-    int before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kTileThreads / 32; ++w) {
-      const int s = warp_sum[w];
-      if (w < warp) before += s;
-      total += s;
-    }
-    int at = base + before + inc - n;
+    const int lo = bounds[threadIdx.x];
+    start = bounds[kTileThreads];
+    const int n = (hi - lo + t.tile_m - 1) / t.tile_m;  // none behind the last expert: hi = lo
+    int at = base + block_scan<false>(n, warp_sum) - n;
     for (int j = 0; j < n; ++j, ++at)
       if (at < t.max_tiles)
         t.tiles[at] = make_int4(e, lo + j * t.tile_m, min(t.tile_m, hi - lo - j * t.tile_m), 0);
-    base += total;
+#pragma unroll
+    for (int w = 0; w < kTileThreads / 32; ++w) base += warp_sum[w];
     __syncthreads();
   }
   if (threadIdx.x == 0) *t.n_mtiles = min(base, t.max_tiles);
