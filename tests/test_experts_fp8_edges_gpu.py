@@ -1,4 +1,5 @@
-"""8-bit routed experts where they can go wrong: offsets that do not ascend."""
+"""8-bit routed experts where they can go wrong: offsets that do not ascend, calls one
+behind the other."""
 import numpy as np
 import pytest
 import torch
@@ -71,3 +72,26 @@ def test_offsets_that_do_not_ascend(tiles, name):
         tol = (L / 32 + 2) * 2.0 ** -23 * (np.abs(av[r]) @ np.abs(wv[e]).T)     # a rounding for each step of 32
         assert (np.abs(out[r] - av[r] @ wv[e].T) <= tol).all(), e
     assert (out[outside] == 7.0).all()
+
+
+def test_calls_one_behind_the_other(tiles):
+    """Products of other shapes in turn, each started beside the end of the one before: the same bits every time."""
+    rng = np.random.default_rng(12)
+    runs = []
+    for n, R, n_in, n_out in ((700, 2, 128, 256), (1500, 3, 640, 264), (300, 1, 2064, 520)):
+        _, a, a_s = quantized(rng.standard_normal((n, n_in)), 1)
+        _, w, w_s = quantized(0.05 * rng.standard_normal((R, n_out, n_in)), 128)
+        d = lm.make_dims(n, 128, 128, R, 1, 0, 128, 0, dtype=torch.float32)
+        off = gpu(np.linspace(0, n, R + 1).astype(np.int32))
+        runs.append((d, a, a_s, off, w, w_s, lm.alloc_workspace(d)))
+
+    def outputs():
+        outs = [torch.empty(r[0].n_tokens, r[4].shape[1], device="cuda") for r in runs]
+        for r, out in zip(runs, outs):
+            lm.moe_expert_gemm_fp8(*r[:6], out, r[6])
+        return outs
+
+    want = outputs()
+    for outs in [outputs() for _ in range(60)]:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert all(lm.get_device_status(r[6]) == lm.OK for r in runs)
