@@ -87,11 +87,12 @@ __device__ __forceinline__ void quantize_vec(const uint4& v, float inv, uint32_t
 // [0, rows]: the offsets themselves where they ascend, as a dispatch gives them,
 // and otherwise still an order in which no row belongs to two experts (two tiles
 // would write it, in either order) and the list fits into max_tiles.  One block
-// of kTileThreads; block-wide scans over as many experts at a time.
+// of kTileThreads, each of which takes some neighbouring experts.
 constexpr int kTileThreads = 256;
-// Inclusive scan over the block; `part` gets the warps' totals.
+// Scan over the block: the result of the threads before this one (MAX: the
+// largest, 0 without any; else the sum).  `part` gets the warps' totals.
 template <bool MAX>
-__device__ __forceinline__ int block_scan(int v, int* part) {
+__device__ __forceinline__ int scan_before(int v, int* part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -100,6 +101,8 @@ __device__ __forceinline__ int block_scan(int v, int* part) {
   }
   if (lane == 31) part[warp] = v;
   __syncthreads();
+  v = __shfl_up_sync(0xffffffffu, v, 1);
+  if (lane == 0) v = 0;
 #pragma unroll
   for (int w = 0; w < kTileThreads / 32; ++w)
     if (w < warp) v = MAX ? max(v, part[w]) : v + part[w];
@@ -107,28 +110,31 @@ __device__ __forceinline__ int block_scan(int v, int* part) {
 }
 __device__ __forceinline__ void build_tile_list(const TileList& t) {
   __shared__ int warp_max[kTileThreads / 32], warp_sum[kTileThreads / 32];
-  __shared__ int bounds[kTileThreads + 1];
-  const int rows = (int)t.rows;
-  int base = 0, start = min(max(t.offsets[0], 0), rows);  // tiles and rows of the experts before
-  for (int e0 = 0; e0 < t.R; e0 += kTileThreads) {
-    const int e = e0 + threadIdx.x;
-    const int end = e < t.R ? min(t.offsets[e + 1], rows) : 0;
-    const int hi = max(start, block_scan<true>(end, warp_max));
-    bounds[threadIdx.x + 1] = hi;
-    if (threadIdx.x == 0) bounds[0] = start;
-    __syncthreads();
-    const int lo = bounds[threadIdx.x];
-    start = bounds[kTileThreads];
-    const int n = (hi - lo + t.tile_m - 1) / t.tile_m;  // none behind the last expert: hi = lo
-    int at = base + block_scan<false>(n, warp_sum) - n;
-    for (int j = 0; j < n; ++j, ++at)
-      if (at < t.max_tiles)
-        t.tiles[at] = make_int4(e, lo + j * t.tile_m, min(t.tile_m, hi - lo - j * t.tile_m), 0);
-#pragma unroll
-    for (int w = 0; w < kTileThreads / 32; ++w) base += warp_sum[w];
-    __syncthreads();
+  const int rows = (int)t.rows, per = (t.R + kTileThreads - 1) / kTileThreads;
+  const int first = min((int)threadIdx.x * per, t.R), last = min(first + per, t.R);
+  auto clamped = [&](int i) { return min(max(t.offsets[i], 0), rows); };
+  int top = threadIdx.x == 0 ? clamped(0) : 0;  // largest of this thread's offsets
+#pragma unroll 4
+  for (int e = first; e < last; ++e) top = max(top, clamped(e + 1));
+  int start = scan_before<true>(top, warp_max);  // first row of this thread's experts
+  if (threadIdx.x == 0) start = clamped(0);
+  int n = 0;
+  for (int e = first, lo = start; e < last; ++e) {
+    const int hi = max(lo, clamped(e + 1));
+    n += (hi - lo + t.tile_m - 1) / t.tile_m;
+    lo = hi;
   }
-  if (threadIdx.x == 0) *t.n_mtiles = min(base, t.max_tiles);
+  int at = scan_before<false>(n, warp_sum);
+  for (int e = first, lo = start; e < last; ++e) {
+    const int hi = max(lo, clamped(e + 1));
+    for (; lo < hi; lo += t.tile_m, ++at)
+      if (at < t.max_tiles) t.tiles[at] = make_int4(e, lo, min(t.tile_m, hi - lo), 0);
+    lo = hi;
+  }
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kTileThreads / 32; ++w) total += warp_sum[w];
+  if (threadIdx.x == 0) *t.n_mtiles = min(total, t.max_tiles);
 }
 __global__ void __launch_bounds__(kTileThreads) expert_tiles_kernel(TileList t) {
   pdl_trigger();
