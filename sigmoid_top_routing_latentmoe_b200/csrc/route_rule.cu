@@ -62,20 +62,16 @@ __device__ __forceinline__ uint32_t warp_sort_desc(uint32_t v) {
   return v;
 }
 
-// The keys are formed with the fast exponential and reciprocal (off by a few
-// 2^-24, as any 32-bit form is; equal logits give equal keys), the weights of
-// the chosen experts with expf and a division.
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
+// Keys take expf and one approximate reciprocal (1 ulp; a score under 2^-126 counts
+// as 0 there), so that a score is as good as any in 32 bits wherever its logit lies;
+// equal logits give equal keys.  (The exponential of a product with log2 e, rounded
+// once, was off by 2^-24 for each unit of |l|: far from zero neighbouring logits
+// changed places.  That took 25 us where this takes 26, 8192 x 896.)  The weights of the chosen experts take a division.
 __device__ __forceinline__ float rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Shared memory of a warp: the keys, group by group (a padding of `lanes` floats
 // after each group keeps the lanes that share a group's scan on different
@@ -139,8 +135,8 @@ constexpr uint32_t kTaken = 0xffffffffu;  // bits of a key that has its slot
 // it (a few dozen) are put in order: each by counting the ones before it, or in
 // k rounds of a warp maximum where k is small.  Clustered keys (more than 64
 // above the bound) and k > 32 take the rounds over every open key.
-// Bound by issue slots (68 %), not bytes: 8192 x 896, top 16, takes 25 us in 14
-// groups and 20 without, 4.7 us at the copy rate; 64 tokens take one warp's chain, 7 us.
+// Bound by issue slots, not bytes: 8192 x 896, top 16, in 14 groups takes 26 us, 4.7
+// at the copy rate; 64 tokens take one warp's chain, 8 us.
 template <bool SOFTMAX, bool GROUPED>
 __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     const float* __restrict__ logits, int64_t ld, const float* __restrict__ bias, int64_t n, int R,
@@ -165,7 +161,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
   uint64_t c0 = 0, c1 = 0;  // this lane's candidates
   float lmax = -INFINITY;   // its largest key (NaN left out)
 
-  float top = 0.0f, inv = 0.0f;  // softmax: the largest logit, 1 / sum of the exponentials
+  float top = 0.0f, den = 0.0f, inv = 0.0f;  // softmax: the largest logit, sum of the exponentials, 1 / sum
   float l0 = -INFINITY, l1 = -INFINITY, bias0 = 0.0f, bias1 = 0.0f;  // small: this lane's
   if (small) {
     if (lane < R) l0 = lr[lane];
@@ -183,18 +179,24 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     }
     top = warp_max(top);
     if (top == -INFINITY) top = 0.0f;  // no expert is open: every score is 0
-    float sum = 0.0f;
     if (small) {
-      sum = ex2((l0 - top) * kLog2e) + ex2((l1 - top) * kLog2e);
+      den = expf(l0 - top) + expf(l1 - top);
     } else {
-#pragma unroll 8
-      for (int e = lane; e < R; e += 32) sum += ex2((lr[e] - top) * kLog2e);  // from L1
+      constexpr int kBatch = 8;
+      for (int e0 = lane; e0 < R; e0 += 32 * kBatch) {  // from L1
+        float l[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) l[j] = e0 + 32 * j < R ? lr[e0 + 32 * j] : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) den += expf(l[j] - top);
+      }
     }
-    sum = warp_sum(sum);
-    inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    den = warp_sum(den);
+    if (den == 0.0f) den = 1.0f;  // every exponential is 0
+    inv = 1.0f / den;
   }
   auto key_of = [&](float l, float b) {
-    return (SOFTMAX ? ex2((l - top) * kLog2e) * inv : rcp(1.0f + ex2(-kLog2e * l))) + b;
+    return (SOFTMAX ? expf(l - top) * inv : rcp(1.0f + expf(-l))) + b;
   };
   auto candidate = [&](float v, int e) { return (uint64_t)key_code(v) << 32 | (uint32_t)~e; };
   if (small) {
@@ -207,22 +209,24 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
       __syncwarp();
     }
   } else {
-    // whole warps of experts without a check, then the rest
-    const float* lj = lr + lane;
-    const float* bj = bias + lane;
-    const int whole = R >> 5, last = whole * 32 + lane;
+    // kBatch keys a lane at a time, their loads in flight together
+    constexpr int kBatch = 7;
     auto put = [&](int e, float v) {
       key[GROUPED ? e + g.group_of(e) * g.lanes : e] = v;
       if (!GROUPED) lmax = fmaxf(lmax, v);
     };
-    if (bias != nullptr) {
-#pragma unroll 7
-      for (int j = 0; j < whole; ++j) put(j * 32 + lane, key_of(lj[j * 32], bj[j * 32]));
-    } else {
-#pragma unroll 7
-      for (int j = 0; j < whole; ++j) put(j * 32 + lane, key_of(lj[j * 32], 0.0f));
+    for (int e0 = lane; e0 < R; e0 += 32 * kBatch) {
+      float l[kBatch], b[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int e = e0 + 32 * j;
+        l[j] = e < R ? lr[e] : 0.0f;
+        b[j] = bias != nullptr && e < R ? bias[e] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (e0 + 32 * j < R) put(e0 + 32 * j, key_of(l[j], b[j]));
     }
-    if (last < R) put(last, key_of(lr[last], bias != nullptr ? bias[last] : 0.0f));
     __syncwarp();
     if (GROUPED) keep_groups(g, key, code, list);
   }
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_rule_kernel(
     float s = 0.0f;
     if (lane < slots) {
       const float l = lr[chosen];
-      s = SOFTMAX ? expf(l - top) * inv : sigmoid_f(l);
+      s = SOFTMAX ? expf(l - top) / den : sigmoid_f(l);
     }
     if (renormalise) sum += warp_sum(s);
     if (lane < slots) {

@@ -1,5 +1,5 @@
-"""Routing under a rule where it can go wrong: a NaN among the chosen experts, calls from
-several host threads at once."""
+"""Routing under a rule where it can go wrong: a NaN among the chosen experts, logits a
+single step apart far from zero, calls from several host threads at once."""
 import ctypes
 import threading
 
@@ -130,3 +130,24 @@ def test_host_threads_side_by_side(grouped):
     for t in threads:
         t.join()
     assert sorted(results) == [(2600, 0, True)] * 2 + [(4096, 0, True)] * 2, results
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_neighbouring_logits_far_from_zero(score):
+    """Two logits one step of fp32 apart, at -8 and beyond, the larger one behind: it comes first.  A step of a
+    logit there is 2^-20 or more and changes its score by that factor; a 32-bit score is off by at most 5 * 2^-24
+    (exponential 2, sum 1, reciprocal 2; softmax: exponential 2, product 1), so the two do not change places."""
+    low = -np.geomspace(8.0, 86.0, 6000).astype(np.float32)
+    n = len(low)
+    near = np.stack([low, np.nextafter(low, np.float32(0.0))], 1)
+    logits = torch.from_numpy(near if score == "sigmoid" else np.concatenate([np.zeros((n, 1), np.float32), near], 1))
+    R = logits.shape[1]
+    ids, _ = route(logits.cuda(), None, R, rule_of(score))
+    want = [1, 0] if score == "sigmoid" else [0, 2, 1]
+    wrong = (ids.cpu().numpy() != np.array(want)).any(1)
+    assert not wrong.any(), (int(wrong.sum()), low[wrong][:5])
+    # the same behind more experts than stay in registers, whose scores are far lower
+    wide = torch.full((n, 96), -200.0)
+    wide[:, 40:40 + R] = logits
+    ids, _ = route(wide.cuda(), None, R, rule_of(score))
+    assert not (ids.cpu().numpy() != 40 + np.array(want)).any()
