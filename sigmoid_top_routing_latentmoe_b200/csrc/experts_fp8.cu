@@ -416,13 +416,19 @@ __device__ __forceinline__ f32x2 up_poly(f32x2 u) {
   return fma2(p, u, both(1.0f));
 }
 // Two SiTU-GLU hidden units beta1 tanh(a / beta1) sigmoid(a) beta2 tanh(c / beta2),
-// in place of a, to a few 2^-24 of their value: a hidden unit is rounded to e4m3
-// next, and a coarser value would fall on the other side of a rounding border
-// more often.  Near zero, tanh(x) = x P(x^2): no cancellation, and
-// beta tanh(a / beta) = a P.  Beyond (WIDE; |x| > kGateX, kUpX), tanh(x) =
+// in place of a, off by at most 25 * 2^-24 of their value for any a and c: a hidden
+// unit is rounded to e4m3 next, and a coarser value would fall on the other side
+// of a rounding border more often.  Near zero, tanh(x) = x P(x^2): no cancellation,
+// and beta tanh(a / beta) = a P.  Beyond (|x| > kGateX, kUpX), tanh(x) =
 // (1 - t) / (1 + t) with t = e^(-2 |x|), its denominator shared with the
-// sigmoid's.
-constexpr float kLog2e = 1.4426950408889634f;
+// sigmoid's.  e^-a = 2^-y, y = a log2 e rounded: off by 2^-24 for each unit of
+// |a|, so beyond kNearA times 1 + r ln 2, r the rest of the exponent.  (For every
+// unit that took the mid layer's gate and up products from 270 to 281 us and moved
+// no hidden unit across a border.)  Past kFarA the sigmoid takes |a| = kFarA: it is
+// 1, or under 2^-126 and 0.  WIDE: some unit of the warp is beyond a bound; the
+// others get the bits that they get without.
+constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147181f;
+constexpr float kNearA = 5.5f, kFarA = 200.0f;
 template <bool WIDE>
 __device__ __forceinline__ void situ_units(float& a0, float& a1, float c0, float c1, float b1,
                                            float b2, float i1, float i2) {
@@ -439,6 +445,11 @@ __device__ __forceinline__ void situ_units(float& a0, float& a1, float c0, float
     for (int i = 0; i < 2; ++i) {
       const float xa = fabsf(av[i] * i1), xc = fabsf(cv[i] * i2);
       const float t1 = ex2(-2.0f * kLog2e * xa), t2 = ex2(-2.0f * kLog2e * xc);
+      if (fabsf(av[i]) > kNearA) {
+        const float s = copysignf(fminf(fabsf(av[i]), kFarA), av[i]), y = s * kLog2e;
+        const float r = fmaf(s, -kLog2eRest, fmaf(s, -kLog2e, y));
+        d[i] = fmaf(ex2(-y), fmaf(r, kLn2, 1.0f), 1.0f);
+      }
       if (xa > kGateX) {
         n[0][i] = copysignf(b1 - b1 * t1, av[i]);
         d[i] *= 1.0f + t1;
@@ -472,7 +483,7 @@ __device__ __forceinline__ void finish_situ(const Params& p, const Tile& tl, flo
       mc = fmaxf(mc, fabsf(v[32 + i]));
     }
     const float i1 = 1.0f / p.beta1, i2 = 1.0f / p.beta2;
-    if (__any_sync(0xffffffffu, ma * i1 > kGateX || mc * i2 > kUpX)) {
+    if (__any_sync(0xffffffffu, ma * i1 > kGateX || mc * i2 > kUpX || ma > kNearA)) {
 #pragma unroll
       for (int i = 0; i < 32; i += 2)
         situ_units<true>(v[i], v[i + 1], v[32 + i], v[33 + i], p.beta1, p.beta2, i1, i2);

@@ -1,5 +1,5 @@
 """8-bit routed experts where they can go wrong: offsets that do not ascend, calls one
-behind the other."""
+behind the other, hidden units next to rounding borders."""
 import numpy as np
 import pytest
 import torch
@@ -9,6 +9,8 @@ import fp8_ref as ref
 pytestmark = pytest.mark.gpu
 
 lm = pytest.importorskip("sigmoid_top_routing_latentmoe_b200")
+
+U = 2.0 ** -24
 
 
 @pytest.fixture(params=["0", "1"], ids=["single", "pairs"])
@@ -95,3 +97,83 @@ def test_calls_one_behind_the_other(tiles):
     for outs in [outputs() for _ in range(60)]:
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert all(lm.get_device_status(r[6]) == lm.OK for r in runs)
+
+
+def border_case(gate, b1, b2, near, rng):
+    """128 up projections c (multiples of 2^-20 below 16) whose hidden units with gate projection `gate` lie `near`
+    roundings above or below the middle between two e4m3 values; the first unit sets the block's scale."""
+    g = b1 * np.tanh(gate / b1) / (1.0 + np.exp(-gate))
+    c = np.empty(128)
+    c[0] = 16.0 - 2.0 ** -20
+    e = int(ref.exponents(abs(g) * b2 * np.tanh(c[0] / b2)))
+    top, least = (abs(g) * b2 * np.tanh(v / b2) * 2.0 ** -e for v in (c[0], 4.0))
+    borders = np.concatenate([(np.arange(8, 16) + 0.5) * 2.0 ** x for x in range(-4, 6)])
+    borders = borders[(borders > 1.001 * least) & (borders < 0.999 * top)]
+    m = rng.choice(borders, 127) * (1.0 + near * U * rng.choice([-1.0, 1.0], 127))
+    c[1:] = np.round(b2 * np.arctanh(m * 2.0 ** e / abs(g) / b2) * 2.0 ** 20) * 2.0 ** -20
+    return c
+
+
+@pytest.mark.parametrize("b1,b2", [(4.0, 25.0), (64.0, 40.0), (2.0, 1e6)])
+def test_hidden_units_next_to_rounding_borders(tiles, b1, b2):
+    """Hidden units beta1 tanh(a / beta1) sigmoid(a) beta2 tanh(c / beta2) for exact a from -80 to 80 and exact c,
+    each some 28 roundings (2^-24) from the middle between two e4m3 values: an activation in 32 bits puts them on
+    the right side.  Its error is at most 25 roundings.  By polynomials (|a| <= 5.5): e^-a 8 (ex2 4, its argument up
+    to 8 4), 1 + e^-a 1, the reciprocal 2, numerators 6 and 4, products 2.  Beyond: e^-a 5 (the argument's rest is
+    made up for), 1 + e^-a 1, denominators 1 + t 2 and their products 2, the reciprocal 2, numerators b - b t 2 and
+    2, t itself (ex2 4, argument 1) 1 and 6 on the quotients at |x| = 1.5 and 0.5, products 2."""
+    rng = np.random.default_rng(7)
+    p, q = rng.integers(8, 16, 60), rng.integers(8, 16, 60)
+    size = p * q * 2.0 ** rng.integers(-6, 0, 60)               # 1 ... 113, four bits by four bits
+    gates = np.where(rng.random(60) < 0.75, -1.0, 1.0) * np.where(size > 80, size / 2, size)
+    R, F, L = len(gates), 128, 384
+    cs = np.stack([border_case(g, b1, b2, 28.0, rng) for g in gates])
+    # gate row: z[256] W_g[256] = a.  up row: six digits of c to the base 16, each in an MMA step of its own
+    z, wg, wu, wo = np.zeros((R, L)), np.zeros((R, F, L)), np.zeros((R, F, L)), np.zeros((R, L, F))
+    mant = np.where(size > 80, 0.5, 1.0) * size / (p * q)
+    z[:, 256], wg[:, :, 256] = np.sign(gates) * p * mant, q[:, None]
+    left = cs.copy()
+    for i in range(6):
+        z[:, 32 * i] = 2.0 ** (-4 * i)
+        wu[:, :, 32 * i] = np.floor(left * 2.0 ** (4 * i))
+        left -= wu[:, :, 32 * i] * z[0, 32 * i]
+    assert (left == 0).all() and wu.max() <= 15
+    wo[:, np.arange(F), np.arange(F)] = 1.0
+    zq = ref.quantize_blocks(z, 1, 128)[2]
+    ws = [quantized(w, 128) for w in (wg, wu, wo)]
+    assert (zq == z).all() and all((v == w).all() for (v, _, _), w in zip(ws, (wg, wu, wo)))
+    h = (b1 * np.tanh(gates / b1) / (1 + np.exp(-gates)))[:, None] * b2 * np.tanh(cs / b2)
+    want_q, want_e, want = ref.quantize_blocks(h, 1, 128)
+    scaled = np.abs(h) * np.exp2(-want_e.astype(float))
+    ulp = np.exp2(np.floor(np.log2(scaled)) - 3)
+    off = np.abs(scaled / ulp - np.floor(scaled / ulp) - 0.5) * ulp / scaled / U
+    assert (off[:, 1:] > 25).all() and (off[:, 1:] < 34).all()
+    d = lm.make_dims(R, 128, L, R, 1, 0, F, 0, beta1=b1, beta2=b2, dtype=torch.float32)
+    work, out = lm.alloc_workspace(d), torch.zeros(R, L, device="cuda")
+    lm.moe_expert_ffn_fp8(d, gpu(z.astype(np.float32)), gpu(np.arange(R, dtype=np.int32)),
+                          gpu(np.arange(R + 1, dtype=np.int32)), *[t for _, q8, s in ws for t in (q8, s)], out, work)
+    assert lm.get_device_status(work) == lm.OK
+    got = out.double().cpu().numpy()
+    wrong = got[:, :F] != want
+    assert not wrong.any(), (int(wrong.sum()), np.unique(gates[wrong.any(1)]))
+    assert (got[:, F:] == 0).all()
+
+
+def test_rows_beside_saturated_ones(tiles):
+    """A row's bits do not depend on the rows beside it: the same alone and among rows whose units saturate."""
+    rng = np.random.default_rng(19)
+    n, L, F = 96, 256, 272
+    z = rng.standard_normal((n, L)).astype(np.float32)
+    wild = z.copy()
+    wild[::2] *= 200.0
+    ws = [quantized(0.08 * rng.standard_normal((1, r, c)), 128) for r, c in ((F, L), (F, L), (L, F))]
+    flat = [t for _, q, s in ws for t in (q, s)]
+    d = lm.make_dims(n, 128, L, 1, 1, 0, F, 0, dtype=torch.float32)
+    outs = []
+    for rows in (z, wild):
+        out, work = torch.zeros(n, L, device="cuda"), lm.alloc_workspace(d)
+        lm.moe_expert_ffn_fp8(d, gpu(rows), gpu(np.arange(n, dtype=np.int32)), gpu(np.array([0, n], np.int32)), *flat,
+                              out, work)
+        outs.append(out)
+    assert torch.equal(outs[0][1::2], outs[1][1::2])
+    assert torch.isfinite(outs[1]).all() and not torch.equal(outs[0][::2], outs[1][::2])
