@@ -1,5 +1,6 @@
 """8-bit routed experts where they can go wrong: offsets that do not ascend, calls one
-behind the other, hidden units next to rounding borders."""
+behind the other, hidden units next to rounding borders, the accumulator
+of the products."""
 import numpy as np
 import pytest
 import torch
@@ -177,3 +178,71 @@ def test_rows_beside_saturated_ones(tiles):
         outs.append(out)
     assert torch.equal(outs[0][1::2], outs[1][1::2])
     assert torch.isfinite(outs[1]).all() and not torch.equal(outs[0][::2], outs[1][::2])
+
+
+def product(a, w):
+    """a w^T and what 32-bit sums may be off by: each MMA adds the 32 products of a step to the accumulator, rounded
+    or cut at 2^-23 of the larger of the accumulator and of the step's magnitudes.  (Random signs keep the
+    accumulator far below the sum of all magnitudes; positive terms do not.)"""
+    acc, tol = np.zeros((len(a), len(w))), 0.0
+    for s in range(0, a.shape[1], 32):
+        at, wt = a[:, s:s + 32], w[:, s:s + 32].T
+        tol = tol + 2 * U * (np.abs(acc) + np.abs(at) @ np.abs(wt))
+        acc = acc + at @ wt
+    return acc, tol
+
+
+@pytest.mark.parametrize("sign", ["either", "positive"])
+@pytest.mark.parametrize("K", [16, 144, 528, 2064, 4096])
+def test_product_keeps_a_32_bit_accumulator(tiles, K, sign):
+    rng = np.random.default_rng(K)
+    x = rng.standard_normal((150, K)) * np.exp(rng.standard_normal((150, 1)))
+    w = rng.standard_normal((2, 264, K)) * 0.02
+    if sign == "positive":
+        x, w = np.abs(x), np.abs(w)
+    av, a, a_s = quantized(x, 1)
+    wv, wq, w_s = quantized(w, 128)
+    offsets = np.array([0, 70, 150], np.int32)
+    d = lm.make_dims(150, 128, 128, 2, 1, 0, 128, 0, dtype=torch.float32)
+    out = torch.empty(150, 264, device="cuda")
+    lm.moe_expert_gemm_fp8(d, a, a_s, gpu(offsets), wq, w_s, out, lm.alloc_workspace(d))
+    got = out.double().cpu().numpy()
+    for e in range(2):
+        r = slice(offsets[e], offsets[e + 1])
+        want, tol = product(av[r], wv[e])
+        assert (np.abs(got[r] - want) <= tol).all(), (np.abs(got[r] - want) / tol).max()
+
+
+@pytest.mark.parametrize("n,L,F,std", [(120, 528, 272, 0.05), (90, 2064, 144, 0.05), (60, 256, 1040, 0.4)])
+def test_ffn_keeps_32_bits(tiles, n, L, F, std):
+    """The FFN with the bounds of `product`: a hidden unit may take the next e4m3 value (or its block the next
+    scale) only where it lies within 25 roundings and the projections' errors of that border.  The gate changes by
+    at most |gate'| da + da^2 (|gate''| < 2), up by at most dc."""
+    rng = np.random.default_rng(L)
+    z = rng.standard_normal((n, L)).astype(np.float32)
+    zq = ref.quantize_blocks(z, 1, 128)[2]
+    ws = [quantized(std * rng.standard_normal((1, r, c)), 128) for r, c in ((F, L), (F, L), (L, F))]
+    (a, da), (c, dc) = (product(zq, v[0]) for v, _, _ in ws[:2])
+    h = ref.situ(a, c, 4.0, 25.0)
+    sig, cap = 1 / (1 + np.exp(-a)), 4.0 * np.tanh(a / 4.0)
+    d_gate = np.abs(sig / np.cosh(a / 4.0) ** 2 + cap * sig * (1 - sig)) * da + da ** 2
+    d_up, up = dc, np.abs(25.0 * np.tanh(c / 25.0))
+    dh = up * d_gate + np.abs(cap * sig) * d_up + d_gate * d_up + 25 * U * np.abs(h)
+    q, e, hq = ref.quantize_blocks(h, 1, 128)
+    s = np.exp2(np.repeat(e, 128, 1)[:, :F].astype(float))
+    ulp = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(h) / s, 2.0 ** -20))), -6) - 3) * s
+    err = np.where(np.abs(np.abs(h - hq) - ulp / 2) <= dh, ulp, 0.0)
+    pad = np.zeros((2, n, e.shape[1] * 128))
+    pad[0, :, :F], pad[1, :, :F] = np.abs(h), dh
+    top, d_top = pad.reshape(2, n, -1, 128).max(3)
+    edge = (ref.exponents(top + d_top) != e) | (ref.exponents(np.maximum(top - d_top, 0)) != e)
+    err = np.where(np.repeat(edge, 128, 1)[:, :F], 2 * ulp, err)
+    assert (err > 0).mean() < 0.01                      # few units are left that open
+    wo = ws[2][0][0]
+    want, tol = product(hq, wo)
+    tol = tol + err @ np.abs(wo).T * (1 + 2 * (F / 32 + 1) * U)
+    d = lm.make_dims(n, 128, L, 1, 1, 0, F, 0, dtype=torch.float32)
+    out, work = torch.zeros(n, L, device="cuda"), lm.alloc_workspace(d)
+    lm.moe_expert_ffn_fp8(d, gpu(z), gpu(np.arange(n, dtype=np.int32)), gpu(np.array([0, n], np.int32)),
+                          *[t for _, q8, sc in ws for t in (q8, sc)], out, work)
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
