@@ -280,7 +280,9 @@ typedef struct {
  * a and c are products with W_g and W_u, the hidden units (in fp32) are
  * quantised, and expert_out is the product with W_o, in the activation dtype.
  * Rows in no expert's range are left as they are; a perm_token entry outside
- * [0, N) counts as a token of zeros.  latent and ff_routed multiples of 16.  z,
+ * [0, N) counts as a token of zeros.  latent and ff_routed multiples of 16;
+ * beta1 and beta2 at least 2^-126 and their product, which bounds the hidden
+ * units, at most 2^126.  z,
  * perm_token, offsets, expert_out and the workspace as for moe_expert_ffn.
  * Both 8-bit products run on CTA pairs (tiles of 256 rows) or single CTAs (128)
  * by the average rows per expert, K and the number of tiles; the environment

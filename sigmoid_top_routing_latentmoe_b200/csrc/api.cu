@@ -1156,6 +1156,10 @@ lmoe_status moe_expert_ffn_fp8(const lmoe_dims* dims, const void* z, const int32
   LMOE_TRY(check_fp8_width(dims->latent, "latent"));
   LMOE_TRY(check_fp8_width(dims->ff_routed, "ff_routed"));
   LMOE_TRY(check_fp8_tiles(dims, std::max(dims->latent, dims->ff_routed)));
+  // Hidden units are smaller than beta1 beta2 and quantised as finite numbers.
+  const float b1 = dims->beta1, b2 = dims->beta2;
+  if (!(std::min(b1, b2) >= 0x1p-126f) || !((double)b1 * b2 <= 0x1p126))
+    return fail(LMOE_EUNSUPPORTED, "beta1, beta2 under 2^-126 or their product over 2^126");
   if (w == nullptr) return fail(LMOE_EINVAL, "weights is NULL");
   if (dims->n_tokens > 0) {
     LMOE_PTR(z, "z");
