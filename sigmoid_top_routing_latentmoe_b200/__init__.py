@@ -278,6 +278,15 @@ def _want(where, *tensors, stream=None):
     return _stream(stream)
 
 
+def _ws_bytes(where, ws):
+    """Bytes of a workspace on the current device."""
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise LmoeError(EINVAL, where, "ws: expected a contiguous CUDA tensor (alloc_workspace)")
+    if ws.get_device() != torch.cuda.current_device():
+        raise LmoeError(EINVAL, where, f"ws is on {ws.device}, not on the current device")
+    return ws.nbytes
+
+
 def _row_stride(where, name, t, shape, dtypes):
     """Row stride of a matrix on the current device whose rows are contiguous and apart."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != torch.cuda.current_device():
@@ -313,12 +322,13 @@ def make_route_rule(score=SCORE_SIGMOID, n_groups=1, topk_groups=1, group_score=
 def moe_route_grouped(dims, rule, x, w_router, expert_bias, ids, probs, ws, stream=None):
     """moe_route under a rule with groups of experts (make_route_rule)."""
     where, act = "moe_route_grouped", _act(dims)
+    ws_bytes = _ws_bytes(where, ws)
     N, R, k = dims.n_tokens, dims.n_routed, dims.top_k
     st = _want(where, ("x", x, (N, dims.d), act), ("w_router", w_router, (R, dims.d), act),
                ("ids", ids, (N, k), torch.int32), ("probs", probs, (N, k), torch.float32),
                *_bias_spec(expert_bias, R), stream=stream)
     _check(_lib.moe_route_grouped(ctypes.byref(dims), ctypes.byref(rule), _ptr(x), _ptr(w_router),
-                                  _ptr(expert_bias), _ptr(ids), _ptr(probs), _ptr(ws), ws.numel(),
+                                  _ptr(expert_bias), _ptr(ids), _ptr(probs), _ptr(ws), ws_bytes,
                                   st), where)
 
 
@@ -390,6 +400,7 @@ def moe_expert_gemm_fp8(dims, a, a_scales, offsets, w, w_scales, out, ws, stream
     """out [N*k, n_out] <- quantised rows a times the quantised weights w [R, n_out, n_in] of
     their expert (offsets=None: one expert that has every row)."""
     where, P, R = "moe_expert_gemm_fp8", dims.n_tokens * dims.top_k, dims.n_routed
+    ws_bytes = _ws_bytes(where, ws)
     _, n_out, n_in = _matrix_dims(where, "w", w, 3)
     st = _want(where, ("a", a, (P, n_in), FP8),
                ("a_scales", a_scales, fp8_row_scales_shape(P, n_in), torch.uint8),
@@ -400,13 +411,14 @@ def moe_expert_gemm_fp8(dims, a, a_scales, offsets, w, w_scales, out, ws, stream
                stream=stream)
     _check(_lib.moe_expert_gemm_fp8(ctypes.byref(dims), n_in, n_out, _ptr(a), _ptr(a_scales),
                                     _ptr(offsets), _ptr(w), _ptr(w_scales), _ptr(out), _ptr(ws),
-                                    ws.numel(), st), where)
+                                    ws_bytes, st), where)
 
 
 def moe_expert_ffn_fp8(dims, z, perm_token, offsets, w_g, w_g_scales, w_u, w_u_scales, w_o,
                        w_o_scales, expert_out, ws, stream=None):
     """moe_expert_ffn with quantised weights (quantize_weights_fp8)."""
     where, P, R = "moe_expert_ffn_fp8", dims.n_tokens * dims.top_k, dims.n_routed
+    ws_bytes = _ws_bytes(where, ws)
     L, F, act = dims.latent, dims.ff_routed, _act(dims)
     in_scales, out_scales = fp8_weight_scales_shape(R, F, L), fp8_weight_scales_shape(R, L, F)
     st = _want(where, ("z", z, (dims.n_tokens, L), act),
@@ -418,7 +430,7 @@ def moe_expert_ffn_fp8(dims, z, perm_token, offsets, w_g, w_g_scales, w_u, w_u_s
                ("expert_out", expert_out, (P, L), act), stream=stream)
     ew = Fp8Experts(*[_ptr(t) for t in (w_g, w_g_scales, w_u, w_u_scales, w_o, w_o_scales)])
     _check(_lib.moe_expert_ffn_fp8(ctypes.byref(dims), _ptr(z), _ptr(perm_token), _ptr(offsets),
-                                   ctypes.byref(ew), _ptr(expert_out), _ptr(ws), ws.numel(), st),
+                                   ctypes.byref(ew), _ptr(expert_out), _ptr(ws), ws_bytes, st),
            where)
 
 
