@@ -87,7 +87,8 @@ __device__ __forceinline__ void quantize_vec(const uint4& v, float inv, uint32_t
 // [0, rows]: the offsets themselves where they ascend, as a dispatch gives them,
 // and otherwise still an order in which no row belongs to two experts (two tiles
 // would write it, in either order) and the list fits into max_tiles.  One block
-// of kTileThreads, each of which takes some neighbouring experts.
+// of kTileThreads, each of which takes some neighbouring experts (one pair of
+// scans: 896 experts 6 us, 9 with a scan for every 256).
 constexpr int kTileThreads = 256;
 // Scan over the block: the result of the threads before this one (MAX: the
 // largest, 0 without any; else the sum).  `part` gets the warps' totals.
@@ -108,33 +109,49 @@ __device__ __forceinline__ int scan_before(int v, int* part) {
     if (w < warp) v = MAX ? max(v, part[w]) : v + part[w];
   return v;
 }
+__device__ __forceinline__ int clamped_offset(const TileList& t, int i) {
+  return min(max(t.offsets[i], 0), (int)t.rows);
+}
+// bound[first] where the offsets do not ascend.
+__device__ __forceinline__ int running_bound(const TileList& t, int first, int last, int* part) {
+  int top = clamped_offset(t, first);
+  for (int e = first; e < last; ++e) top = max(top, clamped_offset(t, e + 1));
+  const int before = scan_before<true>(top, part);
+  __syncthreads();
+  return max(clamped_offset(t, first), before);
+}
 __device__ __forceinline__ void build_tile_list(const TileList& t) {
-  __shared__ int warp_max[kTileThreads / 32], warp_sum[kTileThreads / 32];
-  const int rows = (int)t.rows, per = (t.R + kTileThreads - 1) / kTileThreads;
+  static_assert(kTileM == 128 && kRoutedPairTileM == 256, "tiles of 2^7 or 2^8 rows");
+  __shared__ int part[kTileThreads / 32];
+  const int shift = t.tile_m == kRoutedPairTileM ? 8 : 7;
+  const int per = (t.R + kTileThreads - 1) / kTileThreads;
   const int first = min((int)threadIdx.x * per, t.R), last = min(first + per, t.R);
-  auto clamped = [&](int i) { return min(max(t.offsets[i], 0), rows); };
-  int top = threadIdx.x == 0 ? clamped(0) : 0;  // largest of this thread's offsets
-#pragma unroll 4
-  for (int e = first; e < last; ++e) top = max(top, clamped(e + 1));
-  int start = scan_before<true>(top, warp_max);  // first row of this thread's experts
-  if (threadIdx.x == 0) start = clamped(0);
-  int n = 0;
-  for (int e = first, lo = start; e < last; ++e) {
-    const int hi = max(lo, clamped(e + 1));
-    n += (hi - lo + t.tile_m - 1) / t.tile_m;
+  // this thread's experts: first row, end of the first, whether they ascend
+  int start = t.offsets[first], end = t.offsets[min(first + 1, t.R)];
+  bool ascend = start >= 0 && start <= end && end <= t.rows;
+  for (int e = first + 1, lo = end; e < last; ++e) {
+    const int hi = t.offsets[e + 1];
+    ascend = ascend && lo <= hi && hi <= t.rows;
     lo = hi;
   }
-  int at = scan_before<false>(n, warp_sum);
-  for (int e = first, lo = start; e < last; ++e) {
-    const int hi = max(lo, clamped(e + 1));
+  if (!__syncthreads_and(ascend)) {
+    start = running_bound(t, first, last, part);
+    end = max(start, clamped_offset(t, min(first + 1, t.R)));
+  }
+  int n = 0;  // their tiles
+  for (int e = first, lo = start, hi = end; e < last;) {
+    n += (hi - lo + t.tile_m - 1) >> shift;
+    lo = hi;
+    if (++e < last) hi = max(lo, clamped_offset(t, e + 1));
+  }
+  int at = scan_before<false>(n, part);
+  if (threadIdx.x == kTileThreads - 1) *t.n_mtiles = min(at + n, t.max_tiles);
+  for (int e = first, lo = start, hi = end; e < last;) {
     for (; lo < hi; lo += t.tile_m, ++at)
       if (at < t.max_tiles) t.tiles[at] = make_int4(e, lo, min(t.tile_m, hi - lo), 0);
     lo = hi;
+    if (++e < last) hi = max(lo, clamped_offset(t, e + 1));
   }
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kTileThreads / 32; ++w) total += warp_sum[w];
-  if (threadIdx.x == 0) *t.n_mtiles = min(total, t.max_tiles);
 }
 __global__ void __launch_bounds__(kTileThreads) expert_tiles_kernel(TileList t) {
   pdl_trigger();
