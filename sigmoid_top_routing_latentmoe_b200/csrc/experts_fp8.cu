@@ -129,14 +129,16 @@ struct Sync {
 static_assert(Cfg<1>::SMEM_BYTES + sizeof(Sync) <= 232448 &&
                   Cfg<2>::SMEM_BYTES + sizeof(Sync) <= 232448, "shared memory");
 
-// Waits for the last arrival of the MMA issuer's commits on each barrier of a
-// ring that was left at (stage, phase).  A commit arrives in both CTAs of a pair
-// and is ordered by no cluster barrier: a block that left first could have it
-// land in the shared memory of the next block there.  (A barrier that was never
-// used counts as done.)
+// Before the second CTA of a pair exits: waits for the last arrival of the MMA
+// issuer's commits on each barrier of a ring that was left at (stage, phase).  A
+// commit arrives in both CTAs, ordered by no cluster barrier: a block that left
+// first could have it land in the shared memory of the next block there.  (The
+// leader waits for its last commit itself.  A barrier that was never used counts
+// as done.)
 template <int N>
 __device__ __forceinline__ void last_arrivals(uint64_t* ring, int stage, uint32_t phase, Sync& s,
                                               int32_t* status) {
+#pragma unroll 1
   for (int i = 0; i < N; ++i)
     if (!mbar_wait(smem_u32(&ring[i]), i < stage ? phase : phase ^ 1u, &s.abort_flag, status)) return;
 }
@@ -190,12 +192,12 @@ __device__ void produce(const Params& p, uint32_t ring, Sync& s, Unit u) {
       }
     }
   }
-  // Before the block exits every load issued has landed (a pair's loads land on
-  // the leader's barriers), and so have the arrivals of the MMAs that read them.
-  if (ok) {
+  if (CG == 2 && ok && u.rank != 0) {
     last_arrivals<C::STAGES>(s.empty, stage, phase, s, p.status);
-    if (u.rank != 0) mbar_wait(smem_u32(&s.drain), 0, &s.abort_flag, p.status);
+    mbar_wait(smem_u32(&s.drain), 0, &s.abort_flag, p.status);
   }
+  // every load issued has landed before the block exits (a pair's loads land on
+  // the leader's barriers).
   if (u.rank == 0)
     for (int i = 0; i < C::STAGES; ++i)
       if (issued & (1u << i)) {
@@ -277,7 +279,7 @@ __device__ void feed_scales(const Params& p, uint32_t tmem, Sync& s, Unit u) {
       }
     }
   }
-  last_arrivals<SF_STAGES>(s.sempty, stage, phase, s, p.status);
+  if (CG == 2 && u.rank != 0) last_arrivals<SF_STAGES>(s.sempty, stage, phase, s, p.status);
 }
 
 // The whole warp walks the tiles, so that addresses and descriptors stay in
