@@ -166,7 +166,8 @@ LMOE_API lmoe_status moe_route_logits(const lmoe_dims* dims, const lmoe_route_ru
  * <dprobs, probs> for the routing ids [N, k] (each row k distinct experts, as
  * the forward gives them; an id outside [0, R) adds nothing).  The choice of
  * experts is not differentiated; where sum_T s is at its floor, the floor is a
- * constant.  dlogits shares no element with logits (refused).  Deterministic. */
+ * constant.  dlogits shares no element with logits (refused), and no memory
+ * with ids and dprobs.  Deterministic. */
 LMOE_API lmoe_status moe_route_logits_backward(const lmoe_dims* dims, const lmoe_route_rule* rule,
                                                const float* logits, int64_t ld, const int32_t* ids,
                                                const float* dprobs, float* dlogits, int64_t ld_d,
@@ -233,7 +234,7 @@ LMOE_API lmoe_status moe_expert_ffn(const lmoe_dims* dims, const void* z, const 
  * elements (rows 16-byte aligned); q [rows, cols] and scales out.  With index
  * [rows], row r is x[index[r]], and a row of zeros where index[r] is outside
  * [0, n_src) (the rows of perm_token behind the last sorted pair); without,
- * n_src = rows. */
+ * n_src = rows.  q and scales share no memory with x and index. */
 LMOE_API lmoe_status lmoe_quantize_rows_fp8(const void* x, int32_t dtype, int64_t n_src, int64_t ld,
                                             const int32_t* index, int64_t rows, int32_t cols,
                                             void* q, uint8_t* scales, lmoe_stream stream);

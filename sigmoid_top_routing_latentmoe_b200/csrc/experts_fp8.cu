@@ -47,7 +47,7 @@ constexpr int THREADS = 32 * (SCALE_WARP0 + SCALE_WARPS);
 // The 768 threads start with 80 registers each; the 16 epilogue warps hold 64
 // accumulators a thread and take what the other 8 give up (512 x 96 + 256 x 48
 // = 768 x 80).  Shared memory leaves almost no L1, so a spilled register is read
-// back from L2: the roles are cut so that none spills in its loop.
+// back from L2: the roles are cut to spill little (SiTU 20 bytes, the plain forms none).
 constexpr int REGS_EPI = 96, REGS_OTHER = 48;
 enum Out { OUT_BF16 = 0, OUT_F32 = 1, OUT_SITU = 2 };
 
