@@ -88,7 +88,7 @@ __device__ __forceinline__ void quantize_vec(const uint4& v, float inv, uint32_t
 // and otherwise still an order in which no row belongs to two experts (two tiles
 // would write it, in either order) and the list fits into max_tiles.  One block
 // of kTileThreads, each of which takes some neighbouring experts (one pair of
-// scans: 896 experts 6 us, 9 with a scan for every 256).
+// scans: the quantise step with 896 experts 5.4 us, 7.8 with a scan for every 256).
 constexpr int kTileThreads = 256;
 // Scan over the block: the result of the threads before this one (MAX: the
 // largest, 0 without any; else the sum).  `part` gets the warps' totals.
